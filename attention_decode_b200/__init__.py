@@ -19,10 +19,18 @@ the bookkeeping for sequences decoded in lock-step):
     dc.prefill(k_prompt, v_prompt)
     dc.append(k_new, v_new)          # flushes (quantizes) a full window
     out = dc.attend(q)
+
+A paged 8-bit cache for sequences that grow and end at different times (rows
+of a call packed, the last tokens of their sequences):
+
+    pc = PagedCache.empty(num_pages, Hkv, page_size=64)
+    q  = nsnq_paged_append(k, v, pc, page_table, seq_lens, cu_rows, q=q, rope_base=10000.0)
+    out = nsnq_paged_attn(q, pc, page_table, seq_lens, cu_rows, max_rows, window=4096, sinks=4)
 """
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -44,7 +52,8 @@ EXPORTED = ("nsnq_status_string", "nsnq_last_error", "nsnq_codebook_index_bytes"
             "nsnq_codebook_index_build", "nsnq_encode_workspace", "nsnq_encode", "nsnq_dequant",
             "nsnq_attn_workspace", "nsnq_attn_decode", "nsnq_attn_decode_res",
             "nsnq_attn_decode_rope", "nsnq_residual_write", "nsnq_attn_decode_noalloc",
-            "nsnq_codebook_quantize4", "nsnq_encode_kv_workspace", "nsnq_encode_kv")
+            "nsnq_codebook_quantize4", "nsnq_encode_kv_workspace", "nsnq_encode_kv",
+            "nsnq_paged_append", "nsnq_paged_attn_workspace", "nsnq_paged_attn")
 
 
 class NSNQError(RuntimeError):
@@ -62,6 +71,12 @@ class _Cache(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("shift", ctypes.c_void_p), ("cap", ctypes.c_int64),
                 ("s1_grid", ctypes.c_void_p), ("s1_levels", ctypes.c_void_p)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("status", ctypes.c_void_p)]
 
 
 class _Residual(ctypes.Structure):
@@ -122,6 +137,14 @@ def load(path: str = LIB_PATH):
     L.nsnq_attn_decode_noalloc.restype = ci
     L.nsnq_codebook_quantize4.argtypes = [vp, vp, vp, vp, ci, ci, vp]
     L.nsnq_codebook_quantize4.restype = ci
+    L.nsnq_paged_append.argtypes = [vp, vp, vp, vp, ci, i64, i64, i64, i64, i64, i64, i64, vp, vp,
+                                    ci, ci, ci, ci, ctypes.c_double, _PagedCache, vp, i64, i64, vp]
+    L.nsnq_paged_append.restype = ci
+    L.nsnq_paged_attn_workspace.argtypes = [i64, ci, ci, ci, ci, i64]
+    L.nsnq_paged_attn_workspace.restype = sz
+    L.nsnq_paged_attn.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, ci, ci, ci, ci, _PagedCache,
+                                  vp, i64, i64, i64, i64, ctypes.c_float, vp, ci, vp, sz, vp]
+    L.nsnq_paged_attn.restype = ci
     _lib = L
     return L
 
@@ -544,4 +567,183 @@ def nsnq_attn_decode_rope(q: torch.Tensor, k_cache: Cache, v_cache: Cache, k_cb:
                                         _ptr(out), _dtype_code(out), _ptr(workspace),
                                         workspace.numel() * workspace.element_size(),
                                         _stream(stream)))
+    return out
+
+
+PAGED_BAD_PAGE, PAGED_BAD_LENGTH = 1, 2
+
+
+@dataclasses.dataclass
+class PagedCache:
+    """Keys and values of a layer in pages: k, v [num_pages][Hkv][page_size][D]
+    float8_e4m3fn, k_scales, v_scales [num_pages][Hkv] fp32 (value = code *
+    scale). status is an int32 word in which the kernels report what they left
+    out (PAGED_BAD_PAGE, PAGED_BAD_LENGTH); check() reads it."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+    status: Optional[torch.Tensor] = None
+
+    @property
+    def num_pages(self) -> int:
+        return int(self.k.shape[0])
+
+    @property
+    def heads(self) -> int:
+        return int(self.k.shape[1])
+
+    @property
+    def page_size(self) -> int:
+        return int(self.k.shape[2])
+
+    @classmethod
+    def empty(cls, num_pages: int, H: int, page_size: int = 64, device="cuda", D: int = HEAD_DIM):
+        shape = (num_pages, H, page_size, D)
+        return cls(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                   torch.ones(shape[:2], dtype=torch.float32, device=device),
+                   torch.ones(shape[:2], dtype=torch.float32, device=device),
+                   torch.zeros(1, dtype=torch.int32, device=device))
+
+    def check(self):
+        """Raise if a call since the last check left something out (synchronises
+        with the device); clears the status word."""
+        bits = 0 if self.status is None else int(self.status.item())
+        if bits:
+            self.status.zero_()
+            what = [t for b, t in ((PAGED_BAD_PAGE, "page table entries outside the pool"),
+                                   (PAGED_BAD_LENGTH, "sequence lengths or rows out of range")) if bits & b]
+            raise NSNQError(NSNQ_ERR_INVALID_ARG, "left out by the kernels: " + ", ".join(what))
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_cstruct":
+            object.__setattr__(self, "_cstruct", None)  # the C view no longer matches
+
+    def _c(self) -> _PagedCache:
+        c = getattr(self, "_cstruct", None)
+        if c is None:
+            dev, shape = self.k.device, self.k.shape
+            if self.k.dim() != 4 or self.v.shape != shape or shape[3] != HEAD_DIM:
+                raise ValueError(f"k and v must be [num_pages][Hkv][page_size][{HEAD_DIM}]")
+            if self.k.dtype != torch.float8_e4m3fn or self.v.dtype != torch.float8_e4m3fn:
+                raise TypeError("k and v must be float8_e4m3fn")
+            for t in (self.k_scales, self.v_scales):
+                if t.dtype != torch.float32 or t.shape != shape[:2]:
+                    raise TypeError("scales must be float32 [num_pages][Hkv]")
+            if self.status is not None and (self.status.dtype != torch.int32 or not self.status.numel()):
+                raise TypeError("status must be an int32 tensor")
+            for t in (self.k, self.v, self.k_scales, self.v_scales, self.status):
+                if t is not None and (t.device != dev or not t.is_cuda or not t.is_contiguous()):
+                    raise ValueError("the cache's tensors must be contiguous, on one CUDA device")
+            c = _PagedCache(_ptr(self.k), _ptr(self.v), _ptr(self.k_scales), _ptr(self.v_scales),
+                            self.num_pages, self.page_size, self.heads, _ptr(self.status))
+            object.__setattr__(self, "_cstruct", c)
+        return c
+
+
+def _paged_seqs(dev, B, n_rows, page_table, seq_lens, cu_rows):
+    """Checks of the device arrays that describe a call's sequences."""
+    for name, t, dim in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1), ("cu_rows", cu_rows, 1)):
+        if t is None:
+            continue
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+        if t.dim() != dim or t.device != dev or (t.numel() and t.stride(dim - 1) != 1):
+            raise ValueError(f"{name} must be a {dim}-dimensional tensor on {dev} with contiguous rows")
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table has {page_table.shape[0]} rows for {B} sequences")
+    if cu_rows is None:
+        if n_rows != B:
+            raise ValueError(f"{n_rows} rows for {B} sequences: pass cu_rows")
+    elif cu_rows.shape[0] != B + 1:
+        raise ValueError(f"cu_rows must hold {B + 1} entries")
+
+
+class _OnStream:
+    """The device of a call's tensors made current, and its stream with it, so
+    that what the call allocates belongs to the stream that uses it."""
+
+    def __new__(cls, device, stream):
+        if stream is None:
+            return contextlib.nullcontext() if device.index == torch.cuda.current_device() \
+                else torch.cuda.device(device)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+
+
+def nsnq_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
+                      seq_lens: torch.Tensor, cu_rows: Optional[torch.Tensor] = None,
+                      q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                      rope_base: float = 0.0, stream=None) -> Optional[torch.Tensor]:
+    """Store new keys and values k, v [rows][Hkv][D] (fp32 or bf16) in the cache,
+    the keys rotated to their positions if rope_base is given. Sequence b owns
+    rows [cu_rows[b], cu_rows[b+1]) (one row each without cu_rows), its last
+    tokens: seq_lens[b] counts its tokens with them. page_table [B][columns]
+    lists each sequence's pages. With q [rows][Hq][D], returns q rotated the
+    same way (into q_out if given)."""
+    N, H, D = k.shape
+    c, dev, B = cache._c(), k.device, int(seq_lens.shape[0])
+    if v.shape != k.shape or v.dtype != k.dtype or k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("k and v must have the same shape and dtype and contiguous channels")
+    if dev != cache.k.device or v.device != dev:
+        raise ValueError("k, v and the cache must be on one device")
+    _paged_seqs(dev, B, N, page_table, seq_lens, cu_rows)
+    Hq, qs = H, (0, 0)
+    with _OnStream(dev, stream):
+        if q is not None:
+            if q.dim() != 3 or q.shape[0] != N or q.shape[2] != D or q.dtype != k.dtype or q.stride(2) != 1 \
+                    or q.device != dev:
+                raise ValueError("q must be [rows][Hq][D] like k, with contiguous channels")
+            Hq, qs = int(q.shape[1]), q.stride()
+            if q_out is None:
+                q_out = torch.empty(N, Hq, D, dtype=q.dtype, device=dev)
+            elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous() \
+                    or q_out.device != dev:
+                raise ValueError("q_out must be contiguous, of q's shape and dtype")
+        _check(load().nsnq_paged_append(_ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _dtype_code(k), N,
+                                        k.stride(0), k.stride(1), v.stride(0), v.stride(1), qs[0], qs[1],
+                                        _ptr(cu_rows), _ptr(seq_lens), B, Hq, H, D, float(rope_base), c,
+                                        _ptr(page_table), page_table.shape[1],
+                                        max(page_table.stride(0), page_table.shape[1]), _stream(stream)))
+    return q_out if q is not None else None
+
+
+def nsnq_paged_attn_workspace(n_rows: int, B: int, Hq: int, Hkv: int, max_rows: int, D: int = HEAD_DIM) -> int:
+    return int(load().nsnq_paged_attn_workspace(n_rows, B, Hq, Hkv, D, max_rows))
+
+
+def nsnq_paged_attn(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                    cu_rows: Optional[torch.Tensor] = None, max_rows: int = 1, window: int = 0,
+                    sinks: int = 0, softmax_scale: float = 0.0,
+                    out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of the packed rows q [rows][Hq][D] (rotated, fp32 or bf16),
+    the last tokens of their sequences, over the paged cache: returns
+    [rows][Hq][D]. max_rows bounds the rows of a sequence. With window > 0 a
+    row sees the last `window` tokens up to its own and the first `sinks`."""
+    N, Hq, D = q.shape
+    c, dev, B = cache._c(), q.device, int(seq_lens.shape[0])
+    if q.stride(2) != 1 or dev != cache.k.device:
+        raise ValueError("q must have contiguous channels and be on the cache's device")
+    _paged_seqs(dev, B, N, page_table, seq_lens, cu_rows)
+    with _OnStream(dev, stream):
+        if out is None:
+            out = torch.empty(N, Hq, D, dtype=out_dtype, device=dev)
+        elif out.shape != q.shape or not out.is_contiguous() or out.device != dev:
+            raise ValueError("out must be contiguous, of q's shape")
+        if workspace is None:
+            workspace = _workspace(nsnq_paged_attn_workspace(N, B, Hq, cache.heads, max_rows, D), dev)
+        elif workspace.device != dev:
+            raise ValueError("the workspace must be on the cache's device")
+        _check(load().nsnq_paged_attn(_ptr(q), _dtype_code(q), N, q.stride(0), q.stride(1), _ptr(cu_rows),
+                                      max_rows, _ptr(seq_lens), B, Hq, cache.heads, D, c,
+                                      _ptr(page_table), page_table.shape[1],
+                                      max(page_table.stride(0), page_table.shape[1]), window, sinks,
+                                      float(softmax_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _stream(stream)))
     return out

@@ -384,6 +384,113 @@ nsnq_status nsnq_attn_decode_noalloc(const void* q, nsnq_dtype q_dtype, nsnq_cac
                                      int Hkv, int D, float softmax_scale, void* out,
                                      nsnq_dtype out_dtype, nsnq_stream stream);
 
+/*
+ * Paged 8-bit cache: the keys and values of a layer in pages of page_size
+ * tokens, held in e4m3 with one scale per page and kv-head (value = code *
+ * scale), for sequences that grow and end at different times. It trades the
+ * 1 or 2 bits of the caches above for 8 bits that the tensor cores read
+ * directly, and needs no codebook. One pool serves every sequence; row b of
+ * the page table lists the pages of sequence b, in order: token t lies in
+ * page page_table[b * table_stride + t / page_size], row t % page_size.
+ *  - A page that is written must belong to one sequence; pages that are only
+ *    read may be shared (a common prefix).
+ *  - New rows of a call are packed: sequence b owns rows [cu_rows[b],
+ *    cu_rows[b + 1]) of the row tensors, and they are its last tokens:
+ *    seq_lens[b] counts its tokens WITH them, so row cu_rows[b] + i is token
+ *    seq_lens[b] - (cu_rows[b + 1] - cu_rows[b]) + i. cu_rows = NULL: one row
+ *    per sequence (n_rows = B). Rows outside [cu_rows[0], cu_rows[B]) are
+ *    neither read nor written.
+ *  - cu_rows, seq_lens and page_table are device arrays, so the host cannot
+ *    check them. The kernels never leave a buffer over them: what they find
+ *    wrong they leave out and report in *cache.status (bits or'ed in, never
+ *    cleared by the library).
+ */
+typedef struct {
+    uint8_t* k;         /* device e4m3 [num_pages][heads][page_size][D], 128-byte aligned */
+    uint8_t* v;         /* device e4m3, same layout and alignment */
+    float* k_scales;    /* device fp32 [num_pages][heads] */
+    float* v_scales;    /* device fp32 [num_pages][heads] */
+    int64_t num_pages;  /* num_pages * heads < 2^31 */
+    int page_size;      /* 16, 32, 64 or 128 tokens */
+    int heads;          /* kv-heads */
+    uint32_t* status;   /* device word or NULL: nsnq_paged_status bits */
+} nsnq_paged_cache;
+
+typedef enum {
+    NSNQ_PAGED_BAD_PAGE = 1,   /* a needed page_table entry outside [0, num_pages): its tokens
+                                  were left out (not stored; not seen by attention) */
+    NSNQ_PAGED_BAD_LENGTH = 2  /* a sequence longer than its table row, with more rows than tokens
+                                  or than max_rows, or rows outside [0, n_rows): left out */
+} nsnq_paged_status;
+
+/*
+ * nsnq_paged_append -- store new keys and values in a paged cache, rotating
+ * the keys (and queries) to their positions on the way.
+ *   k, v   device [n_rows][Hkv][D] of dtype with the given row and head
+ *          strides (elements; channels contiguous, rows 16-byte aligned).
+ *   q      device [n_rows][Hq][D] likewise, or NULL: rotated like the keys
+ *          into q_out [n_rows][Hq][D] (contiguous, of dtype; may equal a
+ *          contiguous q), each value rounded once. Hq is ignored without q.
+ *   rope_base  0: no rotation (q_out is then a copy of q). Else finite, > 1:
+ *          (x_i, x_{i+D/2}) -> (x_i c - x_{i+D/2} s, x_i s + x_{i+D/2} c),
+ *          c, s = cos, sin of t * rope_base^(-2i/D), i < D/2, at token t.
+ *   page_table  device int32 [B][table_cols], rows table_stride apart.
+ * Codes are the nearest e4m3 value (ties to even) of x / scale, x the exact
+ * (fp64) rotated value; infinities are held at +-448 * scale, NaN stays NaN.
+ * The scale of a (page, head) is the least power of two 2^e, e >= -126, with
+ * every finite |x| of its tokens <= 448 * 2^e. A page's first token (row 0)
+ * starts its scale afresh, whatever the page held. Tokens appended to a page
+ * that holds older tokens of the sequence keep its scale if they fit under
+ * it; else the scale grows and the page's older codes are rounded again to
+ * the new one (exact but for codes that fall below e4m3's normal range).
+ * Rows behind the new tokens are left as they were. Pages that several
+ * sequences of a call write to are the caller's error (their contents are
+ * then any mix of both).
+ * B, Hq, Hkv <= 65535, n_rows * max(Hq, Hkv) < 2^31 (NSNQ_ERR_UNSUPPORTED
+ * above). Hkv must equal cache.heads. n_rows = 0 or B = 0 is a no-op.
+ */
+nsnq_status nsnq_paged_append(const void* k, const void* v, const void* q, void* q_out,
+                              nsnq_dtype dtype, int64_t n_rows, int64_t k_stride_t,
+                              int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h,
+                              int64_t q_stride_t, int64_t q_stride_h, const int32_t* cu_rows,
+                              const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
+                              double rope_base, nsnq_paged_cache cache, const int32_t* page_table,
+                              int64_t table_cols, int64_t table_stride, nsnq_stream stream);
+
+/* Workspace bytes nsnq_paged_attn needs (0 for arguments it would reject). */
+size_t nsnq_paged_attn_workspace(int64_t n_rows, int B, int Hq, int Hkv, int D, int64_t max_rows);
+
+/*
+ * nsnq_paged_attn -- causal attention of packed query rows over a paged
+ * cache, from one query per sequence (a decode step) through a few (drafted
+ * tokens) to whole prompts and chunks of them behind a context:
+ *   out_r = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q_r . k_t),
+ * over the tokens t that row r (token position pos) sees: t <= pos, and with
+ * window > 0 also t > pos - window or t < sinks (the first `sinks` tokens
+ * stay visible). A row that sees nothing gets zeros.
+ *   q      device [n_rows][Hq][D] of q_dtype, row and head strides in
+ *          elements (channels contiguous, 16-byte aligned), already rotated.
+ *   max_rows  host upper bound on the rows of a sequence.
+ *   window 0: every token up to pos; else >= 1. sinks >= 0, used with window.
+ *   softmax_scale  0 means 1/sqrt(D).
+ *   out    device [n_rows][Hq][D] contiguous, out_dtype.
+ *   workspace  >= nsnq_paged_attn_workspace(...) bytes, 256-byte aligned;
+ *          calls that may run at the same time need one each.
+ * Pages that no row of the call sees are not read and their table entries
+ * may be anything (a window's user frees them). Token rows that a query does
+ * not see never change its result, whatever their bits (NaN codes too).
+ * Query head h reads kv-head h / (Hq / Hkv). cu_rows, seq_lens, page_table
+ * and the limits are those of nsnq_paged_append; every value of the cache's
+ * scales must be finite and positive.
+ */
+nsnq_status nsnq_paged_attn(const void* q, nsnq_dtype q_dtype, int64_t n_rows, int64_t q_stride_t,
+                            int64_t q_stride_h, const int32_t* cu_rows, int64_t max_rows,
+                            const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
+                            nsnq_paged_cache cache, const int32_t* page_table, int64_t table_cols,
+                            int64_t table_stride, int64_t window, int64_t sinks,
+                            float softmax_scale, void* out, nsnq_dtype out_dtype, void* workspace,
+                            size_t workspace_bytes, nsnq_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
