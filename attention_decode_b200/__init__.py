@@ -570,7 +570,7 @@ def nsnq_attn_decode_rope(q: torch.Tensor, k_cache: Cache, v_cache: Cache, k_cb:
     return out
 
 
-PAGED_BAD_PAGE, PAGED_BAD_LENGTH = 1, 2
+PAGED_BAD_PAGE, PAGED_BAD_LENGTH, PAGED_TIMEOUT = 1, 2, 4
 
 
 @dataclasses.dataclass
@@ -578,7 +578,8 @@ class PagedCache:
     """Keys and values of a layer in pages: k, v [num_pages][Hkv][page_size][D]
     float8_e4m3fn, k_scales, v_scales [num_pages][Hkv] fp32 (value = code *
     scale). status is an int32 word in which the kernels report what they left
-    out (PAGED_BAD_PAGE, PAGED_BAD_LENGTH); check() reads it."""
+    out (PAGED_BAD_PAGE, PAGED_BAD_LENGTH) or that a call's outputs are void
+    (PAGED_TIMEOUT); check() reads it."""
     k: torch.Tensor
     v: torch.Tensor
     k_scales: torch.Tensor
@@ -613,7 +614,8 @@ class PagedCache:
         if bits:
             self.status.zero_()
             what = [t for b, t in ((PAGED_BAD_PAGE, "page table entries outside the pool"),
-                                   (PAGED_BAD_LENGTH, "sequence lengths or rows out of range")) if bits & b]
+                                   (PAGED_BAD_LENGTH, "sequence lengths or rows out of range"),
+                                   (PAGED_TIMEOUT, "a wait that passed its limit (outputs void)")) if bits & b]
             raise NSNQError(NSNQ_ERR_INVALID_ARG, "left out by the kernels: " + ", ".join(what))
 
     def __setattr__(self, name, value):

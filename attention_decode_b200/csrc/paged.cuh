@@ -66,7 +66,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__
 
-constexpr uint32_t kBadPage = NSNQ_PAGED_BAD_PAGE, kBadLength = NSNQ_PAGED_BAD_LENGTH;
+constexpr uint32_t kBadPage = NSNQ_PAGED_BAD_PAGE, kBadLength = NSNQ_PAGED_BAD_LENGTH, kTimeout = NSNQ_PAGED_TIMEOUT;
 
 __device__ __forceinline__ void paged_report(const PagedSeqs& s, uint32_t bits) {
     if (s.status && bits) atomicOr(s.status, bits);

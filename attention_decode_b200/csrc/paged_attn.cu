@@ -1,106 +1,645 @@
-// Attention over the paged 8-bit cache.
+// Attention over the paged 8-bit cache for few query rows per kv-head: decode
+// steps and drafted tokens; every row count for fp32 queries or outputs.
 //
-// One block per (row, query head): its four warps take the visible tokens in
-// turn, lane l holding channels [4l, 4l+4), with a running maximum and sum
-// per warp that are joined at the end.
+// The cache's e4m3 codes go to the tensor cores as they are: TMA brings a
+// tile of 128 tokens of K and V into shared memory and tcgen05.mma
+// (kind::f8f6f4) reads it there, so no thread touches a code and the kernel
+// can run at the rate of the memory. What meets the codes has to be e4m3
+// too: a query row and a column of weights are each split into pieces of 4
+// significant bits,
+//   x = sum_k 2^(-5k) e4m3(2^(5k) (x - pieces before)),
+// and every piece is a column of its own. The scores of a tile are
+//   S[token][piece, row] = K q^T   (M = 128 tokens, N = pieces x rows, K = 128 channels),
+// lane t of TMEM holding token t; a thread adds its token's pieces, applies
+// the page's scale, takes p = 2^(s - m), and writes w = p * (v scale / the
+// segment's largest v scale) in pieces; then
+//   O[channel][piece, row] += V^T w   (M = 128 channels, K = 128 tokens).
+// Two pieces hold a bf16 query exactly (8 bits; the row scaled to at most
+// 256, elements below 2^-14 of that lose bits to an absolute 2^-24 of it);
+// three hold weights to 2^-12, six hold fp32 queries and weights to 2^-24.
+// Products of codes are exact in fp32, and fp32 is what TMEM accumulates.
+//
+// The running maximum m of a row may lag by 2^kLag, so that a tile seldom
+// needs it raised: a vote of the 128 token threads per tile decides; sums of
+// p stay per thread until the segment ends. The bias 2^kBias keeps the
+// smallest piece of a weight at 2^-25 of the row's largest weight.
 #include <math.h>
 
 #include "attn_split.cuh"
-#include "paged.cuh"
+#include "paged_plan.cuh"
+#include "umma.cuh"
 
 namespace nsnq {
 
 namespace {
 
-constexpr int kAttnThreads = 128;
+constexpr int kThreads = 192;  // warps 0-3: tokens / channels; 4: TMA; 5: MMA issue
+constexpr float kLag = 3.f, kBias = 5.f;
+constexpr int kMaxSlots = 8;   // pages per tile (page_size 16)
 
-template <typename QT, typename OT>
-__global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
-    __shared__ float sm[4], sl[4], so[4][kD];
+constexpr int pad16(int n) { return (n + 15) / 16 * 16; }
+constexpr int pow2_at_least(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
+
+// RC rows per unit, QP pieces of a query, PP pieces of a weight.
+template <int RC, int QP, int PP>
+struct Shape {
+    static constexpr int N1 = pad16(RC * QP), N2 = pad16(RC * PP);
+    static constexpr int kStages = RC <= 8 && PP <= 3 ? 3 : 2;  // of 32 KB; two CTAs share an SM
+    static constexpr int kTmem = pow2_at_least(2 * N1 + N2);
+    // shared memory, from a 1024-aligned base
+    static constexpr uint32_t kK = 0, kV = kK + kStages * 16384, kQ = kV + kStages * 16384,
+                              kP = kQ + N1 * 128, kMisc = kP + 2 * N2 * 128;
+};
+
+struct Misc {
+    uint64_t full[3], empty[3], s_full[2], s_free[2], p_full[2], p_free[2], q_ready;
+    uint32_t tmem;
+    uint32_t ok[3];               // stage: pages of the tile that were loaded
+    float ks[3][kMaxSlots], vs[3][kMaxSlots];
+    float c[32];                  // row: score scale (softmax scale, log2 e, query scale)
+    float m[32];                  // row: running maximum (log2 units)
+    int pos[32];                  // row: token position
+    float red[4][33];
+    uint32_t nan[32][4];          // row: channels that a NaN code of a partly seen tile reaches
+};
+
+// -- a part of the segment that ends in the workspace: [RC][128] sums, [RC] m, [RC] l --
+template <int RC>
+__host__ __device__ constexpr int part_stride() { return RC * (kD + 2); }
+
+struct MapPair {
+    CUtensorMap k, v;
+};
+
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_rest(uint32_t h, uint32_t c) {  // (h - c) * 32, exact
+    uint32_t r;
+    asm("{.reg .b32 d;\n\tsub.f16x2 d, %1, %2;\n\tmul.f16x2 %0, d, %3;}" : "=r"(r) : "r"(h), "r"(c), "r"(0x50005000u));
+    return r;
+}
+
+__device__ __forceinline__ void store_out(const PagedAttnArgs& a, int64_t row, int d, float v) {
+    if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[row * kD + d] = __float2bfloat16_rn(v);
+    else reinterpret_cast<float*>(a.out)[row * kD + d] = v;
+}
+
+// The pieces of two weights (rows r and r + 1): out[k] holds piece k's two codes.
+template <int PP>
+__device__ __forceinline__ void weight_pieces(float w0, float w1, uint32_t (&out)[PP]) {
+    if constexpr (PP <= 3) {  // 11 bits of fp16 are enough to start from
+        uint32_t h = f16x2(w0, w1);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) {
+            out[k] = e4m3x2_of_f16x2(h);
+            if (k + 1 < PP) h = f16x2_rest(h, e4m3x2_to_f16x2(out[k]));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < PP; ++k) {
+            out[k] = e4m3x2(w0, w1);
+            const uint32_t h = e4m3x2_to_f16x2(out[k]);
+            w0 = (w0 - f16_lo(h)) * 32.f;
+            w1 = (w1 - f16_hi(h)) * 32.f;
+        }
+    }
+}
+
+__device__ __forceinline__ void bar_tokens() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool any_token(bool v) {  // vote of the 128 token threads
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+// Waits until a limit; once a wait has failed, the kernel goes through the
+// motions without waiting (every index is still in bounds) and the call's
+// results are void: it reports that.
+struct Waiter {
+    bool good = true;
+    __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) {
+        if (good) good = mbar_wait(bar, parity);
+    }
+};
+
+template <int RC, int QP, typename QT>
+__device__ __forceinline__ void write_queries(const PagedAttnArgs& a, const PagedUnit& u, int G, uint8_t* q_sm,
+                                              Misc& ms) {
     const int lane = lane_id(), warp = threadIdx.x >> 5;
-    const int64_t r = blockIdx.x / a.Hq;
-    const int hq = (int)(blockIdx.x % a.Hq), h = hq / (a.Hq / a.Hkv);
-    PagedSeq s{};
-    int b = 0;
-    bool mine = false;
-    for (b = 0; b < a.seqs.B; ++b) {
-        s = paged_seq(a.seqs, b);
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            paged_report(a.seqs, s.bad | (s.rows > a.max_rows ? kBadLength : 0u));
-        if (r >= s.row0 && r < s.row0 + s.rows && r - s.row0 < a.max_rows) mine = true;
-        if (mine && blockIdx.x) break;
-    }
-    if (blockIdx.x == 0)
-        for (b = 0; b < a.seqs.B; ++b) {
-            s = paged_seq(a.seqs, b);
-            if (r >= s.row0 && r < s.row0 + s.rows && r - s.row0 < a.max_rows) break;
+    for (int r = warp; r < RC; r += 4) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        int pos = -1;
+        if (r < u.rows) {
+            const int rr = u.r0 + r, i = rr / G, hq = u.h * G + rr - i * G;
+            load4(reinterpret_cast<const QT*>(a.q) + (int64_t)(u.row0 + i) * a.q_st + (int64_t)hq * a.q_sh + 4 * lane, x);
+            pos = u.first_pos + i;
         }
-    if (!mine) return;
-    const int pos = s.len - s.rows + (int)(r - s.row0);
-    float q[4];
-    load4(reinterpret_cast<const QT*>(a.q) + r * a.q_st + hq * a.q_sh + 4 * lane, q);
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
-    const int ns = a.sinks < lo ? a.sinks : lo;  // sinks in front of the window
-    for (int i = warp; i < ns + pos + 1 - lo; i += 4) {
-        const int t = i < ns ? i : i - ns + lo;
-        const int64_t id = a.seqs.table[b * a.seqs.table_stride + t / a.page];
-        if (id < 0 || id >= a.num_pages) {
-            if (lane == 0) paged_report(a.seqs, kBadPage);
-            continue;
+        float top = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            top = fmaxf(top, fabsf(x[k]));
+            bad |= !isfinite(x[k]);
         }
-        const int64_t ph = id * a.Hkv + h;
-        const int64_t at = (ph * a.page + t % a.page) * kD + 4 * lane;
-        const uint32_t kw = *reinterpret_cast<const uint32_t*>(a.kc + at);
-        const uint32_t vw = *reinterpret_cast<const uint32_t*>(a.vc + at);
-        const uint32_t k0 = e4m3x2_to_f16x2(kw & 0xffffu), k1 = e4m3x2_to_f16x2(kw >> 16);
-        float dot = q[0] * f16_lo(k0);
-        dot = fmaf(q[1], f16_hi(k0), dot);
-        dot = fmaf(q[2], f16_lo(k1), dot);
-        dot = fmaf(q[3], f16_hi(k1), dot);
-        const float sc = warp_sum(dot) * (a.ks[ph] * a.scale_log2);
-        const float mn = fmaxf(m, sc);
-        const float f = m == mn ? 1.f : exp2f(m - mn), p = exp2f(sc - mn);
-        m = mn;
-        l = fmaf(l, f, p);
-        const float w = p * a.vs[ph];
-        const uint32_t v0 = e4m3x2_to_f16x2(vw & 0xffffu), v1 = e4m3x2_to_f16x2(vw >> 16);
-        const float v[4] = {f16_lo(v0), f16_hi(v0), f16_lo(v1), f16_hi(v1)};
+        top = warp_max(top);
+        bad = __any_sync(kFull, bad);
+        // the least e >= -126 with top <= 256 * 2^e
+        const uint32_t bits = __float_as_uint(top);
+        int e = (int)(bits >> 23) - 127 - ((bits & 0x7fffffu) ? 7 : 8);
+        e = bad ? 0 : (e < -126 ? -126 : e);
+        const float up = __uint_as_float((uint32_t)(127 - e) << 23), down = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = fmaf(w, v[k], o[k] * f);
+        for (int k = 0; k < 4; ++k) x[k] *= up;
+#pragma unroll
+        for (int k = 0; k < QP; ++k) {
+            const int n = k * RC + r;
+            uint32_t c0 = e4m3x2(x[0], x[1]), c1 = e4m3x2(x[2], x[3]);
+            const uint32_t h0 = e4m3x2_to_f16x2(c0), h1 = e4m3x2_to_f16x2(c1);
+            x[0] = (x[0] - f16_lo(h0)) * 32.f;
+            x[1] = (x[1] - f16_hi(h0)) * 32.f;
+            x[2] = (x[2] - f16_lo(h1)) * 32.f;
+            x[3] = (x[3] - f16_hi(h1)) * 32.f;
+            const uint32_t word = bad ? 0x7f7f7f7fu : (c0 | (c1 << 16));
+            *reinterpret_cast<uint32_t*>(q_sm + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4) = word;
+        }
+        if (lane == 0) {
+            ms.c[r] = a.scale_log2 * down;
+            ms.pos[r] = pos;
+            ms.m[r] = r < u.rows ? -INFINITY : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ms.nan[r][k] = 0u;
+        }
     }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) so[warp][4 * lane + k] = o[k];
+}
+
+template <int RC, int QP, int PP, typename QT>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_cols_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ MapPair maps) {
+    using Sh = Shape<RC, QP, PP>;
+    constexpr int N1 = Sh::N1, N2 = Sh::N2, ST = Sh::kStages;
+    extern __shared__ __align__(1024) uint8_t smraw[];
+    uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(sm);
+    Misc& ms = *reinterpret_cast<Misc*>(sm + Sh::kMisc);
+    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(smem_u32(&ms.full[i]), 33);
+            mbar_init(smem_u32(&ms.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ms.s_full[i]), 1);
+            mbar_init(smem_u32(&ms.s_free[i]), 4);
+            mbar_init(smem_u32(&ms.p_full[i]), 4);
+            mbar_init(smem_u32(&ms.p_free[i]), 1);
+        }
+        mbar_init(smem_u32(&ms.q_ready), 4);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tmem_alloc(smem_u32(&ms.tmem), Sh::kTmem);
+    for (int i = tid; i < (N1 * 128 + 2 * N2 * 128) / 16; i += kThreads)  // padding columns stay zero
+        reinterpret_cast<uint4*>(sm + Sh::kQ)[i] = make_uint4(0, 0, 0, 0);
+    // Stale rows of a partly loaded tile must be finite before the first use.
+    for (int i = tid; i < ST * 16384 / 16; i += kThreads)
+        reinterpret_cast<uint4*>(sm + Sh::kV)[i] = make_uint4(0, 0, 0, 0);
+    proxy_fence();
+    tc_fence_before();
     __syncthreads();
-    const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float total = 0.f, acc = 0.f;
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    PagedWalk<RC> walk(a);
+    const int64_t total = walk.total();
+    const int ctas = plan_ctas(total, gridDim.x);
+    const bool used = (int)blockIdx.x < ctas;
+    const int64_t begin = used ? plan_begin(total, ctas, blockIdx.x) : 0;
+    const int64_t end = used ? plan_begin(total, ctas, blockIdx.x + 1) : 0;
+    const int G = a.Hq / a.Hkv;
+    const int slots = kTile / a.page;
+    if (blockIdx.x == 0 && warp == 4 && a.seqs.status)
+        for (int i = lane; i < a.seqs.B; i += 32) {
+            const PagedSeq q = paged_seq(a.seqs, i);
+            paged_report(a.seqs, q.bad | (q.rows > a.max_rows ? kBadLength : 0u));
+        }
+    Waiter wait;
+    int j0 = begin < end ? walk.seek(begin) : 0;  // first tile of the segment in its unit
+    uint32_t it = 0;                              // tiles of this CTA so far
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ TMA --
+        const int page_log = 31 - __clz(a.page);
+        bool missing = false;
+        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+            const PagedUnit u = walk.u;
+            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            const int32_t* row = a.seqs.table + u.b * a.seqs.table_stride;
+            // this lane's page of a tile, -1 where no row sees it
+            auto fetch = [&](int j) -> int {
+                if (lane >= slots || j >= j1) return -1;
+                const int slot = u.tile(j) * slots + lane, t0 = slot << page_log;
+                if (t0 > u.p1 || (t0 + a.page <= u.lo_tok && t0 >= a.sinks)) return -1;
+                const int id = row[slot];
+                if (id >= 0 && id < a.num_pages) return id;
+                missing = true;
+                return -1;
+            };
+            int id = fetch(j0);
+            for (int j = j0; j < j1; ++j, ++it) {
+                const int next = fetch(j + 1);
+                const uint32_t st = it % ST, full = smem_u32(&ms.full[st]);
+                wait(smem_u32(&ms.empty[st]), ((it / ST) & 1) ^ 1);
+                const unsigned have = __ballot_sync(kFull, id >= 0);
+                if (lane == 0) {
+                    ms.ok[st] = have;
+                    mbar_arrive_tx(full, (uint32_t)__popc(have) * 2u * (uint32_t)a.page * 128u);
+                }
+                __syncwarp();
+                if (id >= 0) {
+                    const int tile = id * a.Hkv + u.h;
+                    const uint32_t off = st * 16384u + (uint32_t)lane * (uint32_t)a.page * 128u;
+                    tma_tile(sb + Sh::kK + off, &maps.k, tile, full);
+                    tma_tile(sb + Sh::kV + off, &maps.v, tile, full);
+                    cp_async4(smem_u32(&ms.ks[st][lane]), a.ks + tile);
+                    cp_async4(smem_u32(&ms.vs[st][lane]), a.vs + tile);
+                }
+                mbar_arrive_cp_async(full);
+                id = next;
+            }
+            x += j1 - j0;
+            if (x < end) walk.next();
+        }
+        if (missing) paged_report(a.seqs, kBadPage);
+        for (uint32_t i = it < ST ? 0 : it - ST; i < it; ++i)  // no copy is in flight at the end
+            wait(smem_u32(&ms.full[i % ST]), (i / ST) & 1);
+    } else if (warp == 5) {
+        // ------------------------------------------------------------ MMA --
+        if (lane == 0) {
+            constexpr uint32_t id_s = mma_idesc(128, N1, false, false);  // K rows x query columns
+            constexpr uint32_t id_o = mma_idesc(128, N2, true, true);    // V^T (channels) x weights
+            uint32_t seg = 0;
+            for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0, ++seg) {
+                const int cnt = end - x < walk.u.n - j0 ? (int)(end - x) : walk.u.n - j0;
+                wait(smem_u32(&ms.q_ready), seg & 1);
+                for (int i = 0; i <= cnt; ++i) {
+                    if (i < cnt) {
+                        const uint32_t t = it + i, st = t % ST;
+                        wait(smem_u32(&ms.full[st]), (t / ST) & 1);
+                        wait(smem_u32(&ms.s_free[t & 1]), ((t >> 1) & 1) ^ 1);
+                        tc_fence_after();
+                        const uint64_t ka = desc_sw128(sb + Sh::kK + st * 16384u, 16, 1024);
+                        const uint64_t qb = desc_sw128(sb + Sh::kQ, 16, 1024);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = sl[w] == 0.f ? 0.f : exp2f(sm[w] - top);
-        total += f * sl[w];
-        acc += sl[w] == 0.f ? 0.f : f * so[w][threadIdx.x];
+                        for (int k = 0; k < 4; ++k)  // 32 channels each
+                            mma_f8(tmem + (t & 1) * N1, ka + 2 * k, qb + 2 * k, id_s, k > 0);
+                        mma_commit(smem_u32(&ms.s_full[t & 1]));
+                    }
+                    if (i > 0) {
+                        const uint32_t t = it + i - 1, st = t % ST;
+                        wait(smem_u32(&ms.p_full[t & 1]), (t >> 1) & 1);
+                        tc_fence_after();
+                        const uint64_t va = desc_sw128(sb + Sh::kV + st * 16384u, 16384, 1024);
+                        const uint64_t pb = desc_plain(sb + Sh::kP + (t & 1) * N2 * 128, 128, 2048);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // 32 tokens each
+                            mma_f8(tmem + 2 * N1, va + 256 * k, pb + 32 * k, id_o, i > 1 || k > 0);
+                        mma_commit(smem_u32(&ms.p_free[t & 1]));
+                        mma_commit(smem_u32(&ms.empty[st]));
+                    }
+                }
+                it += cnt;
+                x += cnt;
+                if (x < end) walk.next();
+            }
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------- tokens, then channels --
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        const int page_log = 31 - __clz(a.page), slot = tid >> page_log;
+        const uint32_t all_slots = (1u << slots) - 1u;
+        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+            const PagedUnit u = walk.u;
+            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            const uint32_t real = u.rows >= 32 ? kFull : (1u << u.rows) - 1u;
+            bar_tokens();  // the segment before is done with the row data
+            write_queries<RC, QP, QT>(a, u, G, sm + Sh::kQ, ms);
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready));
+            bar_tokens();
+            float l[RC], vref = 0.f;
+#pragma unroll
+            for (int r = 0; r < RC; ++r) l[r] = 0.f;
+            for (int j = j0; j < j1; ++j, ++it) {
+                const uint32_t buf = it & 1, st = it % ST;
+                wait(smem_u32(&ms.s_full[buf]), (it >> 1) & 1);
+                wait(smem_u32(&ms.full[st]), (it / ST) & 1);
+                tc_fence_after();
+                float y[RC];
+#pragma unroll
+                for (int r = 0; r < RC; ++r) y[r] = 0.f;
+                constexpr int W = RC * QP % 32 == 0 ? 32 : RC * QP % 16 == 0 ? 16 : 8;  // columns a load
+#pragma unroll
+                for (int c0 = 0; c0 < RC * QP; c0 += W) {
+                    float v[W];
+                    tmem_ld<W>(lanes + buf * N1 + c0, v);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        const int k = (c0 + i) / RC, r = (c0 + i) % RC;
+                        y[r] = k == 0 ? v[i] : fmaf(v[i], 1.f / (float)(1ull << (5 * k)), y[r]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.s_free[buf]));
+                const int tile = u.tile(j), tok = tile * kTile + tid;
+                const uint32_t have = ms.ok[st];
+                const bool whole = have == all_slots && tile * kTile + kTile - 1 <= u.p0 &&
+                                   (!a.window || tile * kTile > u.p1 - a.window || tile * kTile + kTile <= a.sinks);
+                const float ks = ms.ks[st][slot], vs = ms.vs[st][slot];
+                uint32_t vis = kFull;
+                if (!whole) {
+                    vis = 0;
+                    if ((have >> slot) & 1u) {
+                        const int back = a.window && tok >= a.sinks ? a.window : 0x7fffffff;
+#pragma unroll
+                        for (int r = 0; r < RC; ++r) {
+                            const int gap = ms.pos[r] - tok;
+                            vis |= (gap >= 0 && gap < back ? 1u : 0u) << r;
+                        }
+                        vis &= real;
+                    }
+                }
+                float most = -INFINITY;
+#pragma unroll
+                for (int r = 0; r < RC; ++r) {
+                    y[r] *= ks;
+                    const float z = fmaf(y[r], ms.c[r], -ms.m[r]);
+                    if (r < u.rows && ((vis >> r) & 1u)) most = fmaxf(most, z);
+                }
+                if (any_token(most > kLag || (vis != 0 && vs > vref))) {
+                    // raise the maxima: per row over the tile's tokens, and the v scale
+#pragma unroll
+                    for (int r = 0; r < RC; ++r) {
+                        const float z = warp_max((vis >> r) & 1u ? y[r] * ms.c[r] : -INFINITY);
+                        if (lane == 0) ms.red[warp][r] = z;
+                    }
+                    const float top_v = warp_max(vis ? vs : 0.f);
+                    if (lane == 0) ms.red[warp][32] = top_v;
+                    bar_tokens();
+                    const float vn = fmaxf(fmaxf(vref, fmaxf(ms.red[0][32], ms.red[1][32])),
+                                           fmaxf(ms.red[2][32], ms.red[3][32]));
+                    const float fv = vref > 0.f ? vref / vn : 0.f;
+                    vref = vn;
+                    float f[RC];
+#pragma unroll
+                    for (int r = 0; r < RC; ++r) {
+                        const float m = ms.m[r];
+                        const float mn = fmaxf(fmaxf(m, fmaxf(ms.red[0][r], ms.red[1][r])),
+                                               fmaxf(ms.red[2][r], ms.red[3][r]));
+                        f[r] = m == mn ? 1.f : exp2_approx(m - mn);
+                        l[r] *= f[r];
+                    }
+                    if (j > j0) {
+                        wait(smem_u32(&ms.p_free[buf ^ 1]), ((it - 1) >> 1) & 1);
+                        tc_fence_after();
+#pragma unroll
+                        for (int c0 = 0; c0 < RC * PP; c0 += 8) {
+                            float v[8];
+                            tmem_ld<8>(lanes + 2 * N1 + c0, v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] *= f[(c0 + i) % RC] * fv;
+                            tmem_st8(lanes + 2 * N1 + c0, v);
+                        }
+                        tmem_wait_st();
+                    }
+                    bar_tokens();
+                    if (tid < RC)
+                        ms.m[tid] = fmaxf(fmaxf(ms.m[tid], fmaxf(ms.red[0][tid], ms.red[1][tid])),
+                                          fmaxf(ms.red[2][tid], ms.red[3][tid]));
+                    bar_tokens();
+                }
+                const float wv = vis && vref > 0.f ? vs / vref : 0.f;
+                uint32_t word[N2 / 4];
+#pragma unroll
+                for (int i = 0; i < N2 / 4; ++i) word[i] = 0;
+#pragma unroll
+                for (int r = 0; r < RC; r += 2) {
+                    float w[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float p = exp2_approx(fmaf(y[r + i], ms.c[r + i], kBias - ms.m[r + i]));
+                        w[i] = (vis >> (r + i)) & 1u ? p : 0.f;
+                        l[r + i] += w[i];
+                        w[i] *= wv;
+                    }
+                    uint32_t c[PP];
+                    weight_pieces<PP>(w[0], w[1], c);
+#pragma unroll
+                    for (int k = 0; k < PP; ++k) word[(k * RC + r) / 4] |= c[k] << (((k * RC + r) & 2) * 8);
+                }
+                wait(smem_u32(&ms.p_free[buf]), ((it >> 1) & 1) ^ 1);
+#pragma unroll
+                for (int i = 0; i < N2 / 16; ++i)
+                    *reinterpret_cast<uint4*>(sm + Sh::kP + buf * N2 * 128 + i * 2048 + tid * 16) =
+                        make_uint4(word[4 * i], word[4 * i + 1], word[4 * i + 2], word[4 * i + 3]);
+                if (!whole && vis != real) {
+                    // a token that some row does not see: its values must not
+                    // meet that row's zero weight as NaN
+                    uint8_t* vrow = sm + Sh::kV + st * 16384 + tid * 128;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const int pc = (i + lane) & 7;  // spreads the lanes over the banks
+                        uint4* at = reinterpret_cast<uint4*>(vrow + pc * 16);
+                        if (!vis) {
+                            *at = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        uint32_t c[4] = {at->x, at->y, at->z, at->w};
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t nan = __vcmpeq4(c[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            any |= nan;
+                            c[k] &= ~nan;
+                            const int d0 = ((pc ^ (tid & 7)) << 4) + 4 * k;
+                            for (uint32_t left = nan & 0x01010101u; left; left &= left - 1)
+                                for (uint32_t seen = vis; seen; seen &= seen - 1) {
+                                    const int d = d0 + ((__ffs(left) - 1) >> 3);
+                                    atomicOr(&ms.nan[__ffs(seen) - 1][d >> 5], 1u << (d & 31));
+                                }
+                        }
+                        if (any) *at = make_uint4(c[0], c[1], c[2], c[3]);
+                    }
+                }
+                proxy_fence();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.p_full[buf]));
+            }
+            // ---- the segment's rows: sums over the tokens, channels from TMEM ----
+#pragma unroll
+            for (int r = 0; r < RC; ++r) {
+                const float s = warp_sum(l[r]);
+                if (lane == 0) ms.red[warp][r] = s;
+            }
+            wait(smem_u32(&ms.p_free[(it - 1) & 1]), ((it - 1) >> 1) & 1);
+            tc_fence_after();
+            bar_tokens();
+            float o[RC];
+#pragma unroll
+            for (int r = 0; r < RC; ++r) o[r] = 0.f;
+#pragma unroll
+            for (int c0 = 0; c0 < RC * PP; c0 += 8) {
+                float v[8];
+                tmem_ld<8>(lanes + 2 * N1 + c0, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int k = (c0 + i) / RC, r = (c0 + i) % RC;
+                    if (k < PP) o[r] = k == 0 ? v[i] : fmaf(v[i], 1.f / (float)(1ull << (5 * k)), o[r]);
+                }
+            }
+            tc_fence_before();
+            const bool complete = j0 == 0 && j1 == u.n;
+            float* part = a.part + (int64_t)(2 * blockIdx.x + (x == begin ? 0 : 1)) * part_stride<RC>();
+#pragma unroll
+            for (int r = 0; r < RC; ++r) {
+                if (r >= u.rows) continue;
+                const float sum = ms.red[0][r] + ms.red[1][r] + ms.red[2][r] + ms.red[3][r];
+                float v = o[r] * vref;
+                if ((ms.nan[r][tid >> 5] >> (tid & 31)) & 1u) v = NAN;
+                if (!complete) {
+                    part[r * kD + tid] = v;
+                    if (tid == 0) part[RC * kD + r] = ms.m[r], part[RC * kD + RC + r] = sum;
+                    continue;
+                }
+                const int rr = u.r0 + r, i = rr / G;
+                store_out(a, (int64_t)(u.row0 + i) * a.Hq + u.h * G + rr - i * G, tid, sum == 0.f ? 0.f : v / sum);
+            }
+            x += j1 - j0;
+            if (x < end) walk.next();
+        }
     }
-    const float y = total == 0.f ? 0.f : acc / total;
-    const int64_t at = (r * a.Hq + hq) * kD + threadIdx.x;
-    if constexpr (sizeof(OT) == 2) reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
-    else reinterpret_cast<float*>(a.out)[at] = y;
+    if (!wait.good) paged_report(a.seqs, kTimeout);
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, Sh::kTmem);
+}
+
+// Joins the pieces of units that several CTAs worked on, and writes zeros for
+// units that see nothing. One block per (unit, row); thread = channel.
+template <int RC>
+__global__ void __launch_bounds__(kD) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid,
+                                                        int groups) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    PagedWalk<RC> walk(a);
+    int64_t unit = blockIdx.x;
+    const int g = (int)(unit % groups);
+    unit /= groups;
+    walk.h = (int)(unit % a.Hkv);
+    walk.b = (int)(unit / a.Hkv);
+    const PagedSeq s = paged_seq(a.seqs, walk.b);
+    if (g >= walk.group_count(s)) return;
+    const PagedUnit u = walk.unit(s, g);
+    const int r = blockIdx.y, d = threadIdx.x;
+    if (r >= u.rows) return;
+    const int G = walk.G, rr = u.r0 + r, i = rr / G;
+    const int64_t at = (int64_t)(u.row0 + i) * a.Hq + u.h * G + rr - i * G;
+    if (u.n == 0) {
+        store_out(a, at, d, 0.f);
+        return;
+    }
+    const int64_t total = walk.total();
+    const int ctas = plan_ctas(total, grid);
+    const int64_t u0 = walk.before(s, g);
+    const int c0 = plan_cta(total, ctas, u0), c1 = plan_cta(total, ctas, u0 + u.n - 1);
+    if (c0 == c1) return;
+    auto part = [&](int c) {
+        return a.part + (int64_t)(2 * c + (plan_begin(total, ctas, c) >= u0 ? 0 : 1)) * part_stride<RC>();
+    };
+    float top = -INFINITY;
+    for (int c = c0; c <= c1; ++c)
+        if (part(c)[RC * kD + RC + r] != 0.f) top = fmaxf(top, part(c)[RC * kD + r]);
+    float sum = 0.f, acc = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+        const float* p = part(c);
+        const float l = p[RC * kD + RC + r];
+        if (l == 0.f) continue;
+        const float f = exp2_approx(p[RC * kD + r] - top);
+        sum = fmaf(f, l, sum);
+        acc = fmaf(f, p[r * kD + d], acc);
+    }
+    store_out(a, at, d, sum == 0.f ? 0.f : acc / sum);
+}
+
+template <int RC, int QP, int PP, typename QT>
+cudaError_t launch_cols(const PagedAttnArgs& a, cudaStream_t s) {
+    using Sh = Shape<RC, QP, PP>;
+    static std::atomic<unsigned long long> ready{0}, ready_join{0};
+    MapPair maps;
+    cudaError_t e = make_pool_map(&maps.k, a.kc, a.num_pages * a.Hkv, a.page);
+    if (e == cudaSuccess) e = make_pool_map(&maps.v, a.vc, a.num_pages * a.Hkv, a.page);
+    if (e != cudaSuccess) return e;
+    const int ctas = 2 * device_sm_count();
+    e = launch_smem_pdl(paged_cols_kernel<RC, QP, PP, QT>, ready, dim3(ctas), dim3(kThreads),
+                        Sh::kMisc + sizeof(Misc) + 1024, s, a, maps);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = a.max_rows < a.seqs.n_rows ? a.max_rows : a.seqs.n_rows;
+    const int G = a.Hq / a.Hkv;
+    const int64_t pairs = rows * G, groups = (pairs + RC - 1) / RC;
+    const int64_t grid = groups * a.Hkv * a.seqs.B;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    return launch_smem_pdl(paged_join_kernel<RC>, ready_join, dim3((unsigned)grid, (unsigned)(pairs < RC ? pairs : RC)),
+                           dim3(kD), 0, s, a, ctas, (int)groups);
+}
+
+// Rows of a unit: the least power of two that holds a sequence's rows of one
+// kv-head; at most 32, and 8 where fp32 takes six pieces of everything.
+int unit_rows(int64_t pairs, bool f32) {
+    if (pairs <= 4) return 4;
+    if (pairs <= 8 || f32) return 8;
+    return pairs <= 16 ? 16 : 32;
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(int64_t, int, int, int, int64_t) { return 256; }
+size_t paged_attn_workspace(int64_t n_rows, int, int Hq, int Hkv, int64_t max_rows) {
+    const int64_t rows = max_rows < n_rows ? max_rows : n_rows;
+    const int rc = unit_rows(rows * (Hq / Hkv), false);
+    const size_t part = rc <= 8 ? part_stride<8>() : rc == 16 ? part_stride<16>() : part_stride<32>();
+    return (size_t)4 * device_sm_count() * part * sizeof(float);
+}
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
-    const unsigned grid = (unsigned)(a.seqs.n_rows * a.Hq);
-    if (a.q_bf16) {
-        if (a.out_bf16) paged_attn_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kAttnThreads, 0, s>>>(a);
-        else paged_attn_kernel<__nv_bfloat16, float><<<grid, kAttnThreads, 0, s>>>(a);
-    } else {
-        if (a.out_bf16) paged_attn_kernel<float, __nv_bfloat16><<<grid, kAttnThreads, 0, s>>>(a);
-        else paged_attn_kernel<float, float><<<grid, kAttnThreads, 0, s>>>(a);
+    const int64_t rows = a.max_rows < a.seqs.n_rows ? a.max_rows : a.seqs.n_rows;
+    const bool f32 = !a.q_bf16 || !a.out_bf16;
+    const int rc = unit_rows(rows * (a.Hq / a.Hkv), f32);
+    if (f32) {
+        if (a.q_bf16)
+            return rc == 4 ? launch_cols<4, 2, 6, __nv_bfloat16>(a, s) : launch_cols<8, 2, 6, __nv_bfloat16>(a, s);
+        return rc == 4 ? launch_cols<4, 6, 6, float>(a, s) : launch_cols<8, 6, 6, float>(a, s);
     }
-    return cudaGetLastError();
+    switch (rc) {
+        case 4: return launch_cols<4, 2, 3, __nv_bfloat16>(a, s);
+        case 8: return launch_cols<8, 2, 3, __nv_bfloat16>(a, s);
+        case 16: return launch_cols<16, 2, 3, __nv_bfloat16>(a, s);
+        default: return launch_cols<32, 2, 3, __nv_bfloat16>(a, s);
+    }
 }
 
 }  // namespace nsnq

@@ -29,22 +29,22 @@ def _cache(**kw):
 
 def _append(lib, **kw):
     a = dict(k=FAKE, v=OTHER, q=None, qo=None, dt=nsnq.NSNQ_BF16, n=4, kt=256, kh=128, vt=256, vh=128, qt=512,
-             qh=128, cu=FAKE, lens=FAKE, B=2, Hq=4, Hkv=2, D=128, base=10000.0, cache=_cache(), table=FAKE,
+             qh=128, cu=FAKE, lens=FAKE, B=2, Hq=4, Hkv=2, D=128, base=10000.0, cache={}, table=FAKE,
              cols=3, stride=3)
     a.update(kw)
     return lib.nsnq_paged_append(a["k"], a["v"], a["q"], a["qo"], a["dt"], a["n"], a["kt"], a["kh"], a["vt"],
                                  a["vh"], a["qt"], a["qh"], a["cu"], a["lens"], a["B"], a["Hq"], a["Hkv"], a["D"],
-                                 a["base"], a["cache"], a["table"], a["cols"], a["stride"], None)
+                                 a["base"], _cache(**a["cache"]), a["table"], a["cols"], a["stride"], None)
 
 
 def _attn(lib, **kw):
     a = dict(q=FAKE, qd=nsnq.NSNQ_BF16, n=4, qt=512, qh=128, cu=FAKE, mr=3, lens=FAKE, B=2, Hq=4, Hkv=2, D=128,
-             cache=_cache(), table=FAKE, cols=3, stride=3, window=0, sinks=0, scale=0.0, out=FAKE,
+             cache={}, table=FAKE, cols=3, stride=3, window=0, sinks=0, scale=0.0, out=FAKE,
              od=nsnq.NSNQ_BF16, ws=FAKE, wsb=0)
     a.update(kw)
     return lib.nsnq_paged_attn(a["q"], a["qd"], a["n"], a["qt"], a["qh"], a["cu"], a["mr"], a["lens"], a["B"],
-                               a["Hq"], a["Hkv"], a["D"], a["cache"], a["table"], a["cols"], a["stride"],
-                               a["window"], a["sinks"], a["scale"], a["out"], a["od"], a["ws"], a["wsb"], None)
+                               a["Hq"], a["Hkv"], a["D"], _cache(**a["cache"]), a["table"], a["cols"],
+                               a["stride"], a["window"], a["sinks"], a["scale"], a["out"], a["od"], a["ws"], a["wsb"], None)
 
 
 BOTH = [
@@ -54,18 +54,18 @@ BOTH = [
     (dict(B=65536), nsnq.NSNQ_ERR_UNSUPPORTED, b"65535"),
     (dict(n=1 << 30), nsnq.NSNQ_ERR_UNSUPPORTED, b"2^31"),
     (dict(cu=None), nsnq.NSNQ_ERR_INVALID_ARG, b"cu_rows"),
-    (dict(cache=_cache(page=48)), nsnq.NSNQ_ERR_UNSUPPORTED, b"page_size"),
-    (dict(cache=_cache(page=256)), nsnq.NSNQ_ERR_UNSUPPORTED, b"page_size"),
-    (dict(cache=_cache(heads=3)), nsnq.NSNQ_ERR_INVALID_ARG, b"heads"),
-    (dict(cache=_cache(pages=-1)), nsnq.NSNQ_ERR_INVALID_ARG, b"num_pages"),
-    (dict(cache=_cache(pages=1 << 30)), nsnq.NSNQ_ERR_UNSUPPORTED, b"num_pages"),
-    (dict(cache=_cache(k=None)), nsnq.NSNQ_ERR_INVALID_ARG, b"NULL"),
-    (dict(cache=_cache(vs=None)), nsnq.NSNQ_ERR_INVALID_ARG, b"NULL"),
-    (dict(cache=_cache(v=OTHER + 16)), nsnq.NSNQ_ERR_INVALID_ARG, b"128-byte"),
-    (dict(cache=_cache(v=FAKE)), nsnq.NSNQ_ERR_INVALID_ARG, b"share"),
-    (dict(cache=_cache(vs=FAKE)), nsnq.NSNQ_ERR_INVALID_ARG, b"share"),
-    (dict(cache=_cache(ks=FAKE + 2)), nsnq.NSNQ_ERR_INVALID_ARG, b"4-byte"),
-    (dict(cache=_cache(status=FAKE + 1)), nsnq.NSNQ_ERR_INVALID_ARG, b"4-byte"),
+    (dict(cache=dict(page=48)), nsnq.NSNQ_ERR_UNSUPPORTED, b"page_size"),
+    (dict(cache=dict(page=256)), nsnq.NSNQ_ERR_UNSUPPORTED, b"page_size"),
+    (dict(cache=dict(heads=3)), nsnq.NSNQ_ERR_INVALID_ARG, b"heads"),
+    (dict(cache=dict(pages=-1)), nsnq.NSNQ_ERR_INVALID_ARG, b"num_pages"),
+    (dict(cache=dict(pages=1 << 30)), nsnq.NSNQ_ERR_UNSUPPORTED, b"num_pages"),
+    (dict(cache=dict(k=None)), nsnq.NSNQ_ERR_INVALID_ARG, b"NULL"),
+    (dict(cache=dict(vs=None)), nsnq.NSNQ_ERR_INVALID_ARG, b"NULL"),
+    (dict(cache=dict(v=OTHER + 16)), nsnq.NSNQ_ERR_INVALID_ARG, b"128-byte"),
+    (dict(cache=dict(v=FAKE)), nsnq.NSNQ_ERR_INVALID_ARG, b"share"),
+    (dict(cache=dict(vs=FAKE)), nsnq.NSNQ_ERR_INVALID_ARG, b"share"),
+    (dict(cache=dict(ks=FAKE + 2)), nsnq.NSNQ_ERR_INVALID_ARG, b"4-byte"),
+    (dict(cache=dict(status=FAKE + 1)), nsnq.NSNQ_ERR_INVALID_ARG, b"4-byte"),
     (dict(lens=None), nsnq.NSNQ_ERR_INVALID_ARG, b"seq_lens"),
     (dict(table=None), nsnq.NSNQ_ERR_INVALID_ARG, b"page_table"),
     (dict(table=FAKE + 1), nsnq.NSNQ_ERR_INVALID_ARG, b"4-byte"),
