@@ -26,8 +26,7 @@
 #include <math.h>
 
 #include "attn_split.cuh"
-#include "paged_plan.cuh"
-#include "umma.cuh"
+#include "paged_join.cuh"
 
 namespace nsnq {
 
@@ -63,14 +62,6 @@ struct Misc {
     uint32_t nan[32][4];          // row: channels that a NaN code of a partly seen tile reaches
 };
 
-// -- a part of the segment that ends in the workspace: [RC][128] sums, [RC] m, [RC] l --
-template <int RC>
-__host__ __device__ constexpr int part_stride() { return RC * (kD + 2); }
-
-struct MapPair {
-    CUtensorMap k, v;
-};
-
 __device__ __forceinline__ uint32_t f16x2(float a, float b) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
@@ -85,11 +76,6 @@ __device__ __forceinline__ uint32_t f16x2_rest(uint32_t h, uint32_t c) {  // (h 
     uint32_t r;
     asm("{.reg .b32 d;\n\tsub.f16x2 d, %1, %2;\n\tmul.f16x2 %0, d, %3;}" : "=r"(r) : "r"(h), "r"(c), "r"(0x50005000u));
     return r;
-}
-
-__device__ __forceinline__ void store_out(const PagedAttnArgs& a, int64_t row, int d, float v) {
-    if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[row * kD + d] = __float2bfloat16_rn(v);
-    else reinterpret_cast<float*>(a.out)[row * kD + d] = v;
 }
 
 // The pieces of two weights (rows r and r + 1): out[k] holds piece k's two codes.
@@ -124,16 +110,6 @@ __device__ __forceinline__ bool any_token(bool v) {  // vote of the 128 token th
         : "memory");
     return r != 0;
 }
-
-// Waits until a limit; once a wait has failed, the kernel goes through the
-// motions without waiting (every index is still in bounds) and the call's
-// results are void: it reports that.
-struct Waiter {
-    bool good = true;
-    __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) {
-        if (good) good = mbar_wait(bar, parity);
-    }
-};
 
 template <int RC, int QP, typename QT>
 __device__ __forceinline__ void write_queries(const PagedAttnArgs& a, const PagedUnit& u, int G, uint8_t* q_sm,
@@ -541,56 +517,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == 0) tmem_dealloc(tmem, Sh::kTmem);
 }
 
-// Joins the pieces of units that several CTAs worked on, and writes zeros for
-// units that see nothing. One block per (unit, row); thread = channel.
-template <int RC>
-__global__ void __launch_bounds__(kD) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid,
-                                                        int groups) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    PagedWalk<RC> walk(a);
-    int64_t unit = blockIdx.x;
-    const int g = (int)(unit % groups);
-    unit /= groups;
-    walk.h = (int)(unit % a.Hkv);
-    walk.b = (int)(unit / a.Hkv);
-    const PagedSeq s = paged_seq(a.seqs, walk.b);
-    if (g >= walk.group_count(s)) return;
-    const PagedUnit u = walk.unit(s, g);
-    const int r = blockIdx.y, d = threadIdx.x;
-    if (r >= u.rows) return;
-    const int G = walk.G, rr = u.r0 + r, i = rr / G;
-    const int64_t at = (int64_t)(u.row0 + i) * a.Hq + u.h * G + rr - i * G;
-    if (u.n == 0) {
-        store_out(a, at, d, 0.f);
-        return;
-    }
-    const int64_t total = walk.total();
-    const int ctas = plan_ctas(total, grid);
-    const int64_t u0 = walk.before(s, g);
-    const int c0 = plan_cta(total, ctas, u0), c1 = plan_cta(total, ctas, u0 + u.n - 1);
-    if (c0 == c1) return;
-    auto part = [&](int c) {
-        return a.part + (int64_t)(2 * c + (plan_begin(total, ctas, c) >= u0 ? 0 : 1)) * part_stride<RC>();
-    };
-    float top = -INFINITY;
-    for (int c = c0; c <= c1; ++c)
-        if (part(c)[RC * kD + RC + r] != 0.f) top = fmaxf(top, part(c)[RC * kD + r]);
-    float sum = 0.f, acc = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-        const float* p = part(c);
-        const float l = p[RC * kD + RC + r];
-        if (l == 0.f) continue;
-        const float f = exp2_approx(p[RC * kD + r] - top);
-        sum = fmaf(f, l, sum);
-        acc = fmaf(f, p[r * kD + d], acc);
-    }
-    store_out(a, at, d, sum == 0.f ? 0.f : acc / sum);
-}
-
 template <int RC, int QP, int PP, typename QT>
 cudaError_t launch_cols(const PagedAttnArgs& a, cudaStream_t s) {
     using Sh = Shape<RC, QP, PP>;
-    static std::atomic<unsigned long long> ready{0}, ready_join{0};
+    static std::atomic<unsigned long long> ready{0};
     MapPair maps;
     cudaError_t e = make_pool_map(&maps.k, a.kc, a.num_pages * a.Hkv, a.page);
     if (e == cudaSuccess) e = make_pool_map(&maps.v, a.vc, a.num_pages * a.Hkv, a.page);
@@ -599,13 +529,7 @@ cudaError_t launch_cols(const PagedAttnArgs& a, cudaStream_t s) {
     e = launch_smem_pdl(paged_cols_kernel<RC, QP, PP, QT>, ready, dim3(ctas), dim3(kThreads),
                         Sh::kMisc + sizeof(Misc) + 1024, s, a, maps);
     if (e != cudaSuccess) return e;
-    const int64_t rows = a.max_rows < a.seqs.n_rows ? a.max_rows : a.seqs.n_rows;
-    const int G = a.Hq / a.Hkv;
-    const int64_t pairs = rows * G, groups = (pairs + RC - 1) / RC;
-    const int64_t grid = groups * a.Hkv * a.seqs.B;
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_smem_pdl(paged_join_kernel<RC>, ready_join, dim3((unsigned)grid, (unsigned)(pairs < RC ? pairs : RC)),
-                           dim3(kD), 0, s, a, ctas, (int)groups);
+    return launch_paged_join<RC>(a, ctas, s);
 }
 
 // Rows of a unit: the least power of two that holds a sequence's rows of one
@@ -622,7 +546,9 @@ size_t paged_attn_workspace(int64_t n_rows, int, int Hq, int Hkv, int64_t max_ro
     const int64_t rows = max_rows < n_rows ? max_rows : n_rows;
     const int rc = unit_rows(rows * (Hq / Hkv), false);
     const size_t part = rc <= 8 ? part_stride<8>() : rc == 16 ? part_stride<16>() : part_stride<32>();
-    return (size_t)4 * device_sm_count() * part * sizeof(float);
+    const size_t cols = (size_t)4 * device_sm_count() * part * sizeof(float);
+    const size_t whole = paged_rows_workspace();
+    return rows * (Hq / Hkv) > 32 && whole > cols ? whole : cols;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
@@ -634,6 +560,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
             return rc == 4 ? launch_cols<4, 2, 6, __nv_bfloat16>(a, s) : launch_cols<8, 2, 6, __nv_bfloat16>(a, s);
         return rc == 4 ? launch_cols<4, 6, 6, float>(a, s) : launch_cols<8, 6, 6, float>(a, s);
     }
+    if (rows * (a.Hq / a.Hkv) > 32) return launch_paged_rows(a, s);
     switch (rc) {
         case 4: return launch_cols<4, 2, 3, __nv_bfloat16>(a, s);
         case 8: return launch_cols<8, 2, 3, __nv_bfloat16>(a, s);

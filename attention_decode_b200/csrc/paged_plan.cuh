@@ -36,7 +36,8 @@ template <int RC>
 struct PagedWalk {
     const PagedAttnArgs& a;
     PagedSeq s;
-    int G, b, h, g, groups;
+    int G, b = 0, h = 0, g = 0, groups = 0;
+    int64_t first_chunk = 0;  // this lane's sequence of the first 32: its tiles for one kv-head
     PagedUnit u;
 
     __device__ __forceinline__ explicit PagedWalk(const PagedAttnArgs& args) : a(args), G(args.Hq / args.Hkv) {}
@@ -65,28 +66,57 @@ struct PagedWalk {
         v.g = gi;
         return v;
     }
-    // Tiles of all units of a sequence and one kv-head.
-    __device__ __forceinline__ int64_t head_tiles(const PagedSeq& q) const {
-        const int n = group_count(q);
+    // This lane's sequence of chunk b0 .. b0 + 31: the tiles of its units for one
+    // kv-head. Every lane of the warp calls it together. Sequences of a few
+    // groups are summed by their lane, longer ones by the warp (a prompt has
+    // tens of groups and may be the only sequence).
+    __device__ __forceinline__ int64_t head_tiles(int b0) const {
+        constexpr int kFew = 2;
+        const int lane = lane_id();
+        PagedSeq q{};
+        int n = 0;
+        if (b0 + lane < a.seqs.B) {
+            q = paged_seq(a.seqs, b0 + lane);
+            n = group_count(q);
+        }
         int64_t t = 0;
-        for (int i = 0; i < n; ++i) t += unit(q, i).n;
+        if (n <= kFew)
+            for (int i = 0; i < n; ++i) t += unit(q, i).n;
+        for (unsigned many = __ballot_sync(kFull, n > kFew); many; many &= many - 1) {
+            const int src = __ffs(many) - 1;
+            PagedSeq o;
+            o.row0 = 0;
+            o.rows = __shfl_sync(kFull, q.rows, src);
+            o.len = __shfl_sync(kFull, q.len, src);
+            const int m = __shfl_sync(kFull, n, src);
+            int64_t part = 0;
+            for (int i = lane; i < m; i += 32) part += unit(o, i).n;
+#pragma unroll
+            for (int k = 16; k; k >>= 1) part += __shfl_xor_sync(kFull, part, k);
+            if (lane == src) t = part;
+        }
         return t;
     }
     // Tiles of all sequences. Every lane of the warp calls it together.
-    __device__ __forceinline__ int64_t total() const {
+    __device__ __forceinline__ int64_t total() {
         int64_t t = 0;
-        for (int i = lane_id(); i < a.seqs.B; i += 32) t += head_tiles(paged_seq(a.seqs, i));
+        for (int b0 = 0; b0 < a.seqs.B; b0 += 32) {
+            const int64_t mine = head_tiles(b0);
+            if (b0 == 0) first_chunk = mine;
+            t += mine;
+        }
 #pragma unroll
         for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(kFull, t, m);
         return t * a.Hkv;
     }
-    // Goes to the unit that holds tile x < total(); returns the tile's number in it.
+    // Goes to the unit that holds tile x < total(), which was called before;
+    // returns the tile's number in it. Every lane of the warp calls it together.
     __device__ __forceinline__ int seek(int64_t x) {
         const int lane = lane_id();
-        int64_t before = 0, per_head = 0;
+        int64_t before = 0, per_head = 1;
         b = 0;
         for (int b0 = 0; b0 < a.seqs.B; b0 += 32) {
-            const int64_t mine = b0 + lane < a.seqs.B ? head_tiles(paged_seq(a.seqs, b0 + lane)) : 0;
+            const int64_t mine = b0 ? head_tiles(b0) : first_chunk;
             int64_t incl = mine * a.Hkv;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
@@ -107,23 +137,25 @@ struct PagedWalk {
         groups = group_count(s);
         h = (int)(x / per_head);
         x -= h * per_head;
-        for (g = 0;; ++g) {
-            u = unit(s, g);
-            if (x < u.n || g + 1 >= groups) return (int)x;
-            x -= u.n;
-        }
-    }
-    // Tiles of all units in front of unit (b, h, gi) of sequence q = b. Every lane
-    // of the warp calls it together.
-    __device__ __forceinline__ int64_t before(const PagedSeq& q, int gi) const {
-        int64_t t = 0;
-        for (int i = lane_id(); i < b; i += 32) t += head_tiles(paged_seq(a.seqs, i));
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int mine = g0 + lane < groups ? unit(s, g0 + lane).n : 0;
+            int64_t incl = mine;
 #pragma unroll
-        for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(kFull, t, m);
-        t *= a.Hkv;
-        if (h) t += h * head_tiles(q);
-        for (int i = 0; i < gi; ++i) t += unit(q, i).n;
-        return t;
+            for (int m = 1; m < 32; m <<= 1) {
+                const int64_t o = __shfl_up_sync(kFull, incl, m);
+                if (lane >= m) incl += o;
+            }
+            const unsigned hit = __ballot_sync(kFull, x < incl);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                g = g0 + src;
+                x -= __shfl_sync(kFull, incl, src) - __shfl_sync(kFull, mine, src);
+                break;
+            }
+            x -= __shfl_sync(kFull, incl, 31);
+        }
+        u = unit(s, g);
+        return (int)x;
     }
     // The next unit that has tiles; past the last one, u.n = 0.
     __device__ __forceinline__ void next() {

@@ -1,0 +1,542 @@
+// Attention over the paged 8-bit cache for many query rows: prompts, and
+// chunks of prompts behind a context (bf16 queries and outputs).
+//
+// A unit is 256 (query row, head) pairs of one sequence and kv-head, heads
+// fastest, in two halves of 128 rows; a row is a TMEM lane and one thread's.
+// Per tile of 128 tokens and half:
+//   S = Q K^T      tcgen05.mma kind::f8f6f4: K as the cache holds it, Q as two
+//                  e4m3 pieces of 4 significant bits in one accumulator (a bf16
+//                  query scaled to at most 448 is their sum, up to 2^-10),
+//   p = 2^(s - m)  one thread per row: no value crosses a thread,
+//   O += P V       kind::f16, P from TMEM (over S), V widened to fp16 (exact)
+//                  in shared memory by a warpgroup of its own.
+// fp16 weights keep 11 bits; the running maximum may lag by 2^kLag and the
+// bias 2^kBias keeps the largest below 2^14 and the smallest at 2^-30.
+//
+// What bounds it: the tensor cores (2 x 512 clocks per half and tile) and the
+// exponentials (16384 per half and tile, 16 a clock: 1024 clocks). The halves
+// take turns: while one half's weights are computed, the tensor cores work
+// for the other (P V of the tile before, then S of the next).
+#include <math.h>
+
+#include "f32x2.cuh"
+#include "paged_join.cuh"
+
+namespace nsnq {
+
+namespace {
+
+constexpr int RC = 256;         // rows of a unit
+constexpr int kThreads = 512;   // warps 0-3, 4-7: rows; 8-11: V to fp16; 12: TMA; 13: MMA issue
+// Registers a thread of each warpgroup: together the 512 x 128 of the launch.
+constexpr int kRowRegs = 184, kValueRegs = 80, kIssueRegs = 64;
+static_assert(2 * kRowRegs + kValueRegs + kIssueRegs == 4 * 128, "register split");
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+constexpr float kLag = 8.f, kBias = 6.f;
+constexpr int kKStages = 3, kRing = 8;
+constexpr int kMaxSlots = 8;
+
+// shared memory, from a 1024-aligned base
+constexpr uint32_t kQ = 0;                        // [half][piece][128 rows][128 B]
+constexpr uint32_t kK = kQ + 4 * 16384;           // [stage][128 tokens][128 B]
+constexpr uint32_t kV = kK + kKStages * 16384;    // [2][128 tokens][128 B]
+constexpr uint32_t kV16 = kV + 2 * 16384;         // [2][channel half][128 tokens][128 B]
+constexpr uint32_t kMisc = kV16 + 4 * 16384;
+
+struct Misc {
+    uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2], w_full[2], w_free[2], sc_full[kRing];
+    uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];
+    uint32_t tmem;
+    uint32_t ok[kRing];                // pages of the tile that were loaded
+    float2 scale[kRing][kMaxSlots];    // (k scale, v scale) of a page
+    uint32_t nan[RC][4];               // row: channels that a NaN code of a partly seen tile reaches
+};
+
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// One row's query as two e4m3 pieces; returns its scale.
+__device__ __forceinline__ float write_row(const PagedAttnArgs& a, const __nv_bfloat16* q, bool real, uint8_t* hi,
+                                           int row) {
+    uint8_t* lo = hi + 16384;
+    float top = 0.f;
+    bool bad = false;
+    if (real) {
+#pragma unroll 4
+        for (int i = 0; i < kD / 4; ++i) {
+            float x[4];
+            load4(q + 4 * i, x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                top = fmaxf(top, fabsf(x[k]));
+                bad |= !isfinite(x[k]);
+            }
+        }
+    }
+    // the least e >= -126 with top <= 448 * 2^e
+    const uint32_t bits = __float_as_uint(top);
+    int e = (int)(bits >> 23) - 127 - ((bits & 0x7fffffu) > 0x600000u ? 7 : 8);
+    e = bad ? 0 : (e < -126 ? -126 : e);
+    float up = __uint_as_float((uint32_t)(127 - e) << 23);
+    if (a.scale_log2 < 0.f) up = -up;
+    for (int c = 0; c < 8; ++c) {
+        uint32_t h[4] = {0, 0, 0, 0}, l[4] = {0, 0, 0, 0};
+        if (real) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x[4];
+                load4(q + 16 * c + 4 * i, x);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] *= up;
+                const uint32_t c0 = e4m3x2(x[0], x[1]), c1 = e4m3x2(x[2], x[3]);
+                const uint32_t h0 = e4m3x2_to_f16x2(c0), h1 = e4m3x2_to_f16x2(c1);
+                h[i] = bad ? 0x7f7f7f7fu : (c0 | (c1 << 16));
+                l[i] = bad ? 0u : (e4m3x2(x[0] - f16_lo(h0), x[1] - f16_hi(h0)) |
+                                   (e4m3x2(x[2] - f16_lo(h1), x[3] - f16_hi(h1)) << 16));
+            }
+        }
+        const int at = row * 128 + ((c ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+    return fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// A row's view of a tile: columns up to hi and above lo, or below sink, on
+// pages that were loaded.
+struct View {
+    int hi, lo, sink;
+    uint32_t ok;
+    int page_log;
+    __device__ __forceinline__ static uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; }
+    __device__ __forceinline__ uint32_t bits(int c0) const {  // of columns c0 .. c0 + 31
+        uint32_t b = below(hi + 1 - c0) & (~below(lo + 1 - c0) | below(sink - c0));
+        if (!((ok >> (c0 >> page_log)) & 1u)) b &= 0xffff0000u;
+        if (!((ok >> ((c0 + 16) >> page_log)) & 1u)) b &= 0xffffu;
+        return b;
+    }
+};
+
+// Weights of a row over a tile, packed in fp16 pairs; `most` is the largest
+// exponent met (bias in), `sum` the sum of p.
+template <bool MASKED>
+__device__ __forceinline__ void row_weights(uint32_t s, const float2* scale, int page_log, float c, float m, float rv,
+                                            const View& view, uint32_t (&p)[64], float& most, float& sum) {
+    uint64_t acc = pk2(0.f, 0.f);
+    most = -INFINITY;
+    const uint64_t nm = pk2(kBias - m, kBias - m);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float v[32];
+        tmem_ld<32>(s + 32 * q, v);
+        const uint32_t seen = MASKED ? view.bits(32 * q) : kFull;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const float2 kv = scale[(32 * q + 16 * g) >> page_log];
+            const float f = kv.x * c, w = kv.y * rv;
+            const uint64_t f2 = pk2(f, f), w2 = pk2(w, w);
+            const bool weigh = w != 1.f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const int at = 16 * g + i;
+                float2 x = upk2(fma2(pk2(v[at], v[at + 1]), f2, nm));
+                if (MASKED) {
+                    x.x = (seen >> at) & 1u ? x.x : -INFINITY;
+                    x.y = (seen >> at) & 2u ? x.y : -INFINITY;
+                }
+                most = fmaxf(most, fmaxf(x.x, x.y));
+                v[at] = exp2_approx(x.x);
+                v[at + 1] = exp2_approx(x.y);
+                acc = add2(acc, pk2(v[at], v[at + 1]));
+            }
+            if (weigh) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const int at = 16 * g + i;
+                    float2 y = upk2(mul2(pk2(v[at], v[at + 1]), w2));
+                    if (MASKED) {  // the scale of a page that was not loaded is void
+                        y.x = (seen >> at) & 1u ? y.x : 0.f;
+                        y.y = (seen >> at) & 2u ? y.y : 0.f;
+                    }
+                    v[at] = y.x;
+                    v[at + 1] = y.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) p[(32 * q + 16 * g + i) / 2] = f16x2(v[16 * g + i], v[16 * g + i + 1]);
+        }
+    }
+    const float2 t = upk2(acc);
+    sum = t.x + t.y;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_rows_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ MapPair maps) {
+    extern __shared__ __align__(1024) uint8_t smraw[];
+    uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(sm);
+    Misc& ms = *reinterpret_cast<Misc*>(sm + kMisc);
+    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(smem_u32(&ms.k_full[i]), 1);
+            mbar_init(smem_u32(&ms.k_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ms.v_full[i]), 1);
+            mbar_init(smem_u32(&ms.v_empty[i]), 4);
+            mbar_init(smem_u32(&ms.w_full[i]), 4);
+            mbar_init(smem_u32(&ms.w_free[i]), 1);
+            mbar_init(smem_u32(&ms.q_ready[i]), 4);
+            mbar_init(smem_u32(&ms.s_full[i]), 1);
+            mbar_init(smem_u32(&ms.p_full[i]), 4);
+            mbar_init(smem_u32(&ms.o_full[i]), 1);
+        }
+        for (int i = 0; i < kRing; ++i) mbar_init(smem_u32(&ms.sc_full[i]), 33);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tmem_alloc(smem_u32(&ms.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem;  // columns: S of half 0, S of half 1, O of half 0, O of half 1
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    PagedWalk<RC> walk(a);
+    const int64_t total = walk.total();
+    const int ctas = plan_ctas(total, gridDim.x);
+    const bool used = (int)blockIdx.x < ctas;
+    const int64_t begin = used ? plan_begin(total, ctas, blockIdx.x) : 0;
+    const int64_t end = used ? plan_begin(total, ctas, blockIdx.x + 1) : 0;
+    const int G = a.Hq / a.Hkv, slots = kTile / a.page, page_log = 31 - __clz(a.page);
+    if (blockIdx.x == 0 && warp == 12 && a.seqs.status)
+        for (int i = lane; i < a.seqs.B; i += 32) {
+            const PagedSeq q = paged_seq(a.seqs, i);
+            paged_report(a.seqs, q.bad | (q.rows > a.max_rows ? kBadLength : 0u));
+        }
+    Waiter wait;
+    int j0 = begin < end ? walk.seek(begin) : 0;  // first tile of the segment in its unit
+    uint32_t it = 0;                              // tiles of this CTA so far
+
+    if (warp >= 12) {
+        regs_dec<kIssueRegs>();
+        if (warp == 12) {
+        // ------------------------------------------------------------ TMA --
+        bool missing = false;
+        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+            const PagedUnit u = walk.u;
+            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            const int32_t* row = a.seqs.table + u.b * a.seqs.table_stride;
+            auto fetch = [&](int j) -> int {  // this lane's page of a tile, -1 where no row sees it
+                if (lane >= slots || j >= j1) return -1;
+                const int slot = u.tile(j) * slots + lane, t0 = slot << page_log;
+                if (t0 > u.p1 || (t0 + a.page <= u.lo_tok && t0 >= a.sinks)) return -1;
+                const int id = row[slot];
+                if (id >= 0 && id < a.num_pages) return id;
+                missing = true;
+                return -1;
+            };
+            int id = fetch(j0);
+            for (int j = j0; j < j1; ++j, ++it) {
+                const int next = fetch(j + 1);
+                const uint32_t ks = it % kKStages, vs = it & 1, ring = it % kRing;
+                const uint32_t k_full = smem_u32(&ms.k_full[ks]), v_full = smem_u32(&ms.v_full[vs]);
+                const unsigned have = __ballot_sync(kFull, id >= 0);
+                const uint32_t bytes = (uint32_t)__popc(have) * (uint32_t)a.page * 128u;
+                const uint32_t off = (uint32_t)lane * (uint32_t)a.page * 128u;
+                const int tile = id * a.Hkv + u.h;
+                wait(smem_u32(&ms.k_empty[ks]), ((it / kKStages) & 1) ^ 1);
+                if (lane == 0) {
+                    mbar_arrive_tx(k_full, bytes);
+                    ms.ok[ring] = have;
+                    mbar_arrive(smem_u32(&ms.sc_full[ring]));
+                }
+                __syncwarp();
+                if (id >= 0) {
+                    tma_tile(sb + kK + ks * 16384u + off, &maps.k, tile, k_full);
+                    cp_async4(smem_u32(&ms.scale[ring][lane].x), a.ks + tile);
+                    cp_async4(smem_u32(&ms.scale[ring][lane].y), a.vs + tile);
+                }
+                mbar_arrive_cp_async(smem_u32(&ms.sc_full[ring]));
+                wait(smem_u32(&ms.v_empty[vs]), ((it >> 1) & 1) ^ 1);
+                if (lane == 0) mbar_arrive_tx(v_full, bytes);
+                __syncwarp();
+                if (id >= 0) tma_tile(sb + kV + vs * 16384u + off, &maps.v, tile, v_full);
+                id = next;
+            }
+            x += j1 - j0;
+            if (x < end) walk.next();
+        }
+        if (missing) paged_report(a.seqs, kBadPage);
+        for (uint32_t i = it < 3 ? 0 : it - 3; i < it; ++i)  // no copy is in flight at the end
+            wait(smem_u32(&ms.k_full[i % kKStages]), (i / kKStages) & 1);
+        for (uint32_t i = it < 2 ? 0 : it - 2; i < it; ++i) wait(smem_u32(&ms.v_full[i & 1]), (i >> 1) & 1);
+        } else if (warp == 13) {
+        // ------------------------------------------------------------ MMA --
+        if (lane == 0) {
+            constexpr uint32_t id_s = mma_idesc(128, 128, false, false), id_o = mma_idesc(128, 128, false, true);
+            uint32_t seg[2] = {0, 0}, np[2] = {0, 0};  // segments and weight tiles of each half
+            for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+                const int cnt = end - x < walk.u.n - j0 ? (int)(end - x) : walk.u.n - j0;
+                const int halves = walk.u.rows > 128 ? 2 : 1;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                    if (hf < halves) wait(smem_u32(&ms.q_ready[hf]), seg[hf]++ & 1);
+                for (int i = 0; i <= cnt; ++i) {
+                    const uint32_t t = it + i, tp = t - 1;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if (hf >= halves) continue;
+                        if (i > 0) {
+                            if (hf == 0) wait(smem_u32(&ms.w_full[tp & 1]), (tp >> 1) & 1);
+                            wait(smem_u32(&ms.p_full[hf]), np[hf]++ & 1);
+                            tc_fence_after();
+                            const uint64_t vb = desc_sw128(sb + kV16 + (tp & 1) * 32768u, 16384, 1024);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)  // 16 tokens each
+                                mma_f16_ts(tmem + 256 + hf * 128, tmem + hf * 128 + 8 * k, vb + 128 * k, id_o,
+                                           i > 1 || k > 0);
+                            if (i == cnt) mma_commit(smem_u32(&ms.o_full[hf]));
+                        }
+                        if (i < cnt) {
+                            if (hf == 0) {
+                                wait(smem_u32(&ms.k_full[t % kKStages]), (t / kKStages) & 1);
+                                tc_fence_after();
+                            }
+                            const uint64_t kb = desc_sw128(sb + kK + (t % kKStages) * 16384u, 16, 1024);
+                            const uint64_t qa = desc_sw128(sb + kQ + hf * 32768u, 16, 1024);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)  // 32 channels each; the pieces one after the other
+                                mma_f8(tmem + hf * 128, qa + (k >> 2) * 1024 + 2 * (k & 3), kb + 2 * (k & 3), id_s, k > 0);
+                            mma_commit(smem_u32(&ms.s_full[hf]));
+                        }
+                    }
+                    if (i > 0) mma_commit(smem_u32(&ms.w_free[tp & 1]));
+                    if (i < cnt) mma_commit(smem_u32(&ms.k_empty[t % kKStages]));
+                }
+                it += cnt;
+                x += cnt;
+                if (x < end) walk.next();
+            }
+        }
+        __syncwarp();
+        }
+    } else if (warp >= 8) {
+        // -------------------------------------------------- V to fp16 tiles --
+        regs_dec<kValueRegs>();
+        const int tok = tid - 256;  // token of the tile
+        uint32_t seg[2] = {0, 0};
+        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+            const PagedUnit u = walk.u;
+            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            wait(smem_u32(&ms.q_ready[0]), seg[0]++ & 1);  // the rows' NaN marks are clear
+            if (u.rows > 128) wait(smem_u32(&ms.q_ready[1]), seg[1]++ & 1);
+            for (int j = j0; j < j1; ++j, ++it) {
+                const uint32_t buf = it & 1, ring = it % kRing;
+                wait(smem_u32(&ms.sc_full[ring]), (it / kRing) & 1);
+                wait(smem_u32(&ms.v_full[buf]), (it >> 1) & 1);
+                wait(smem_u32(&ms.w_free[buf]), ((it >> 1) & 1) ^ 1);
+                const int t = u.tile(j) * kTile + tok;
+                const bool have = (ms.ok[ring] >> (tok >> page_log)) & 1u;
+                const bool sink = t < a.sinks;
+                const bool some = have && t <= u.p1 && (!a.window || sink || t >= u.p0 || t > u.p0 - a.window);
+                const bool all = have && t <= u.p0 && (!a.window || sink || t > u.p1 - a.window);
+                const uint8_t* src = sm + kV + buf * 16384 + tok * 128;
+                uint8_t* dst = sm + kV16 + buf * 32768 + tok * 128;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {  // 16 channels each
+                    uint4 q = *reinterpret_cast<const uint4*>(src + ((c ^ (tok & 7)) << 4));
+                    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                    if (!all) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (!some) w[k] = 0;
+                            const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            w[k] &= ~nan;
+                            for (uint32_t left = nan & 0x01010101u; left; left &= left - 1) {
+                                const int d = 16 * c + 4 * k + ((__ffs(left) - 1) >> 3);
+                                for (int r = 0; r < u.rows; ++r) {
+                                    const int gap = u.first_pos + (u.r0 + r) / G - t;
+                                    if (gap >= 0 && (!a.window || sink || gap < a.window))
+                                        atomicOr(&ms.nan[r][d >> 5], 1u << (d & 31));
+                                }
+                            }
+                        }
+                    }
+                    uint8_t* half = dst + (c >> 2) * 16384;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint4*>(half + (((2 * (c & 3) + k) ^ (tok & 7)) << 4)) =
+                            make_uint4(e4m3x2_to_f16x2(w[2 * k] & 0xffffu), e4m3x2_to_f16x2(w[2 * k] >> 16),
+                                       e4m3x2_to_f16x2(w[2 * k + 1] & 0xffffu), e4m3x2_to_f16x2(w[2 * k + 1] >> 16));
+                }
+                proxy_fence();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&ms.w_full[buf]));
+                    mbar_arrive(smem_u32(&ms.v_empty[buf]));
+                }
+            }
+            x += j1 - j0;
+            if (x < end) walk.next();
+        }
+    } else {
+        // ------------------------------------------------------------ rows --
+        regs_inc<kRowRegs>();
+        const int hf = warp >> 2, lrow = tid & 127, r = tid;  // r: row of the unit
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + hf * 128, o_at = tmem + lanes + 256 + hf * 128;
+        const uint32_t all_slots = (1u << slots) - 1u;
+        uint32_t n = 0, seg = 0;  // weight tiles and segments of this half
+        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+            const PagedUnit u = walk.u;
+            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            if (hf * 128 < u.rows) {
+                const bool real = r < u.rows;
+                const int rr = u.r0 + (real ? r : 0), qi = rr / G;
+                const int64_t out_row = (int64_t)(u.row0 + qi) * a.Hq + u.h * G + rr - qi * G;
+                const int pos = real ? u.first_pos + qi : -1;
+                // least and largest position of the warp's rows
+                const int w0 = u.r0 + 32 * warp;
+                const int wn = u.rows - 32 * warp < 32 ? u.rows - 32 * warp : 32;
+                const int wp0 = u.first_pos + w0 / G, wp1 = u.first_pos + (w0 + (wn > 0 ? wn : 1) - 1) / G;
+                const float c = write_row(a, reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                 (int64_t)(u.row0 + qi) * a.q_st + (int64_t)(u.h * G + rr - qi * G) * a.q_sh,
+                                          real, sm + kQ + hf * 32768, lrow);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ms.nan[r][k] = 0u;
+                proxy_fence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready[hf]));
+                float m = real ? -INFINITY : 0.f, l = 0.f, vref = 0.f, rv = 0.f;
+                for (int j = j0; j < j1; ++j, ++it, ++n) {
+                    const uint32_t ring = it % kRing;
+                    wait(smem_u32(&ms.s_full[hf]), n & 1);
+                    wait(smem_u32(&ms.sc_full[ring]), (it / kRing) & 1);
+                    tc_fence_after();
+                    const int t0 = u.tile(j) * kTile;
+                    const uint32_t ok = ms.ok[ring];
+                    const float2* scale = ms.scale[ring];
+                    const bool whole = ok == all_slots && t0 + kTile - 1 <= wp0 &&
+                                       (!a.window || t0 > wp1 - a.window || t0 + kTile <= a.sinks);
+                    const View view{pos - t0, a.window ? pos - t0 - a.window : -1, a.sinks - t0, ok, page_log};
+                    float vmax = 0.f;
+                    for (int i = 0; i < slots; ++i)
+                        if ((ok >> i) & 1u) vmax = fmaxf(vmax, scale[i].y);
+                    uint32_t p[64];
+                    float most, sum;
+#pragma unroll 1
+                    for (bool raised = false;; raised = true) {
+                        if (whole) row_weights<false>(s_at, scale, page_log, c, m, rv, view, p, most, sum);
+                        else row_weights<true>(s_at, scale, page_log, c, m, rv, view, p, most, sum);
+                        if (raised || !__any_sync(kFull, (real && most > kBias + kLag) || vmax > vref)) break;
+                        // raise the maxima and the v scale of the warp's rows
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            float v[32];
+                            tmem_ld<32>(s_at + 32 * q, v);
+                            const uint32_t seen = view.bits(32 * q);
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                const float f = scale[(32 * q + 16 * g) >> page_log].x * c;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if ((seen >> (16 * g + i)) & 1u) top = fmaxf(top, v[16 * g + i] * f);
+                            }
+                        }
+                        const float mn = real ? fmaxf(m, top) : 0.f, vn = fmaxf(vref, vmax);
+                        const float f = m == mn ? 1.f : exp2_approx(m - mn);
+                        const float fo = vref > 0.f ? f * (vref / vn) : 0.f;
+                        m = mn;
+                        l *= f;
+                        vref = vn;
+                        rv = vn > 0.f ? 1.f / vn : 0.f;
+                        if (j > j0) {  // P V of the tile before is complete: S came after it
+#pragma unroll 1
+                            for (int q = 0; q < 4; ++q) {
+                                float v[32];
+                                uint32_t w[32];
+                                tmem_ld<32>(o_at + 32 * q, v);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i] * fo);
+                                tmem_st32(o_at + 32 * q, w);
+                            }
+                        }
+                    }
+                    l += sum;
+                    tmem_st32(s_at, p);
+                    tmem_st32(s_at + 32, p + 32);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ms.p_full[hf]));
+                }
+                wait(smem_u32(&ms.o_full[hf]), seg++ & 1);
+                tc_fence_after();
+                const bool complete = j0 == 0 && j1 == u.n;
+                float* part = a.part + (2 * blockIdx.x + (x == begin ? 0 : 1)) * part_stride<RC>();
+                const float inv = complete ? (l == 0.f ? 0.f : vref / l) : vref;
+                __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + out_row * kD;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    float v[32];
+                    tmem_ld<32>(o_at + 32 * q, v);
+                    const uint32_t nan = ms.nan[r][q];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = (nan >> i) & 1u ? NAN : v[i] * inv;
+                    if (!real) continue;
+                    if (complete) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = (uint32_t)f32_to_bf16_rn(v[i + 2 * k]) | ((uint32_t)f32_to_bf16_rn(v[i + 2 * k + 1]) << 16);
+                            *reinterpret_cast<uint4*>(out + 32 * q + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4*>(part + r * kD + 32 * q + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    }
+                }
+                if (!complete && real) part[RC * kD + r] = m, part[RC * kD + RC + r] = l;
+                tc_fence_before();
+            } else {
+                it += j1 - j0;
+            }
+            x += j1 - j0;
+            if (x < end) walk.next();
+        }
+    }
+    if (!wait.good) paged_report(a.seqs, kTimeout);
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+size_t paged_rows_workspace() { return (size_t)2 * device_sm_count() * part_stride<RC>() * sizeof(float); }
+
+cudaError_t launch_paged_rows(const PagedAttnArgs& a, cudaStream_t s) {
+    static std::atomic<unsigned long long> ready{0};
+    MapPair maps;
+    cudaError_t e = make_pool_map(&maps.k, a.kc, a.num_pages * a.Hkv, a.page);
+    if (e == cudaSuccess) e = make_pool_map(&maps.v, a.vc, a.num_pages * a.Hkv, a.page);
+    if (e != cudaSuccess) return e;
+    const int ctas = device_sm_count();
+    e = launch_smem_pdl(paged_rows_kernel, ready, dim3(ctas), dim3(kThreads), kMisc + sizeof(Misc) + 1024, s, a, maps);
+    if (e != cudaSuccess) return e;
+    return launch_paged_join<RC>(a, ctas, s);
+}
+
+}  // namespace nsnq
