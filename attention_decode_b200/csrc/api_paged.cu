@@ -169,7 +169,8 @@ nsnq_status nsnq_paged_attn(const void* q, nsnq_dtype q_dtype, int64_t n_rows, i
     const float scale = softmax_scale == 0.f ? 1.0f / sqrtf((float)D) : softmax_scale;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = out; a.out_bf16 = out_dtype == NSNQ_BF16;
-    a.part = static_cast<float*>(workspace);
+    a.G = nsnq::make_fastdiv((uint32_t)(Hq / Hkv));
+    a.workspace = workspace;
     const cudaError_t e = nsnq::launch_paged_attn(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return set_error(NSNQ_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
     return ok();

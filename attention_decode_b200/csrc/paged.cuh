@@ -59,6 +59,9 @@ struct PagedAttnArgs {
     float scale_log2;
     void* out;
     int out_bf16;
+    FastDiv G;                // query heads per kv-head
+    void* workspace;
+    struct PagedSeam* seams;  // set by the launchers: one per CTA, then the parts
     float* part;
 };
 size_t paged_attn_workspace(int64_t n_rows, int B, int Hq, int Hkv, int64_t max_rows);

@@ -53,6 +53,7 @@ struct Shape {
 struct Misc {
     uint64_t full[3], empty[3], s_full[2], s_free[2], p_full[2], p_free[2], q_ready;
     uint32_t tmem;
+    PagedRange range;
     uint32_t ok[3];               // stage: pages of the tile that were loaded
     float ks[3][kMaxSlots], vs[3][kMaxSlots];
     float c[32];                  // row: score scale (softmax scale, log2 e, query scale)
@@ -112,14 +113,16 @@ __device__ __forceinline__ bool any_token(bool v) {  // vote of the 128 token th
 }
 
 template <int RC, int QP, typename QT>
-__device__ __forceinline__ void write_queries(const PagedAttnArgs& a, const PagedUnit& u, int G, uint8_t* q_sm,
+__device__ __forceinline__ void write_queries(const PagedAttnArgs& a, const PagedUnit& u, int h, uint8_t* q_sm,
                                               Misc& ms) {
+    const int G = (int)a.G.d;
     const int lane = lane_id(), warp = threadIdx.x >> 5;
+#pragma unroll 1
     for (int r = warp; r < RC; r += 4) {
         float x[4] = {0.f, 0.f, 0.f, 0.f};
         int pos = -1;
         if (r < u.rows) {
-            const int rr = u.r0 + r, i = rr / G, hq = u.h * G + rr - i * G;
+            const int rr = u.r0 + r, i = (int)fdiv((uint32_t)rr, a.G), hq = h * G + rr - i * G;
             load4(reinterpret_cast<const QT*>(a.q) + (int64_t)(u.row0 + i) * a.q_st + (int64_t)hq * a.q_sh + 4 * lane, x);
             pos = u.first_pos + i;
         }
@@ -173,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
 
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < ST; ++i) {
             mbar_init(smem_u32(&ms.full[i]), 33);
             mbar_init(smem_u32(&ms.empty[i]), 1);
@@ -187,9 +191,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tmem_alloc(smem_u32(&ms.tmem), Sh::kTmem);
+#pragma unroll 1
     for (int i = tid; i < (N1 * 128 + 2 * N2 * 128) / 16; i += kThreads)  // padding columns stay zero
         reinterpret_cast<uint4*>(sm + Sh::kQ)[i] = make_uint4(0, 0, 0, 0);
     // Stale rows of a partly loaded tile must be finite before the first use.
+#pragma unroll 1
     for (int i = tid; i < ST * 16384 / 16; i += kThreads)
         reinterpret_cast<uint4*>(sm + Sh::kV)[i] = make_uint4(0, 0, 0, 0);
     proxy_fence();
@@ -200,31 +206,35 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    PagedWalk<RC> walk(a);
-    const int64_t total = walk.total();
-    const int ctas = plan_ctas(total, gridDim.x);
-    const bool used = (int)blockIdx.x < ctas;
-    const int64_t begin = used ? plan_begin(total, ctas, blockIdx.x) : 0;
-    const int64_t end = used ? plan_begin(total, ctas, blockIdx.x + 1) : 0;
-    const int G = a.Hq / a.Hkv;
+    if (warp == 0) {
+        const PagedRange r = paged_plan<RC>(a, gridDim.x, blockIdx.x);
+        if (lane == 0) ms.range = r;
+    }
+    __syncthreads();
+    const int64_t begin = ms.range.begin, end = ms.range.end;
+    int j0 = ms.range.j0;  // first tile of the segment in its unit
+    PagedWalk<RC> walk(a, ms.range);
+    if (begin >= end) walk.u.n = 0;
+    const int G = (int)a.G.d;
     const int slots = kTile / a.page;
     if (blockIdx.x == 0 && warp == 4 && a.seqs.status)
+#pragma unroll 1
         for (int i = lane; i < a.seqs.B; i += 32) {
             const PagedSeq q = paged_seq(a.seqs, i);
             paged_report(a.seqs, q.bad | (q.rows > a.max_rows ? kBadLength : 0u));
         }
     Waiter wait;
-    int j0 = begin < end ? walk.seek(begin) : 0;  // first tile of the segment in its unit
-    uint32_t it = 0;                              // tiles of this CTA so far
+    uint32_t it = 0;  // tiles of this CTA so far
 
     if (warp == 4) {
         // ------------------------------------------------------------ TMA --
         const int page_log = 31 - __clz(a.page);
         bool missing = false;
+#pragma unroll 1
         for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
             const PagedUnit u = walk.u;
             const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
-            const int32_t* row = a.seqs.table + u.b * a.seqs.table_stride;
+            const int32_t* row = a.seqs.table + walk.b * a.seqs.table_stride;
             // this lane's page of a tile, -1 where no row sees it
             auto fetch = [&](int j) -> int {
                 if (lane >= slots || j >= j1) return -1;
@@ -236,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 return -1;
             };
             int id = fetch(j0);
+#pragma unroll 1
             for (int j = j0; j < j1; ++j, ++it) {
                 const int next = fetch(j + 1);
                 const uint32_t st = it % ST, full = smem_u32(&ms.full[st]);
@@ -247,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 __syncwarp();
                 if (id >= 0) {
-                    const int tile = id * a.Hkv + u.h;
+                    const int tile = id * a.Hkv + walk.h;
                     const uint32_t off = st * 16384u + (uint32_t)lane * (uint32_t)a.page * 128u;
                     tma_tile(sb + Sh::kK + off, &maps.k, tile, full);
                     tma_tile(sb + Sh::kV + off, &maps.v, tile, full);
@@ -261,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (x < end) walk.next();
         }
         if (missing) paged_report(a.seqs, kBadPage);
+#pragma unroll 1
         for (uint32_t i = it < ST ? 0 : it - ST; i < it; ++i)  // no copy is in flight at the end
             wait(smem_u32(&ms.full[i % ST]), (i / ST) & 1);
     } else if (warp == 5) {
@@ -269,9 +281,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             constexpr uint32_t id_s = mma_idesc(128, N1, false, false);  // K rows x query columns
             constexpr uint32_t id_o = mma_idesc(128, N2, true, true);    // V^T (channels) x weights
             uint32_t seg = 0;
+#pragma unroll 1
             for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0, ++seg) {
                 const int cnt = end - x < walk.u.n - j0 ? (int)(end - x) : walk.u.n - j0;
                 wait(smem_u32(&ms.q_ready), seg & 1);
+#pragma unroll 1
                 for (int i = 0; i <= cnt; ++i) {
                     if (i < cnt) {
                         const uint32_t t = it + i, st = t % ST;
@@ -309,12 +323,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const int page_log = 31 - __clz(a.page), slot = tid >> page_log;
         const uint32_t all_slots = (1u << slots) - 1u;
+#pragma unroll 1
         for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
             const PagedUnit u = walk.u;
             const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
             const uint32_t real = u.rows >= 32 ? kFull : (1u << u.rows) - 1u;
             bar_tokens();  // the segment before is done with the row data
-            write_queries<RC, QP, QT>(a, u, G, sm + Sh::kQ, ms);
+            write_queries<RC, QP, QT>(a, u, walk.h, sm + Sh::kQ, ms);
             proxy_fence();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready));
@@ -322,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float l[RC], vref = 0.f;
 #pragma unroll
             for (int r = 0; r < RC; ++r) l[r] = 0.f;
+#pragma unroll 1
             for (int j = j0; j < j1; ++j, ++it) {
                 const uint32_t buf = it & 1, st = it % ST;
                 wait(smem_u32(&ms.s_full[buf]), (it >> 1) & 1);
@@ -455,7 +471,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                             any |= nan;
                             c[k] &= ~nan;
                             const int d0 = ((pc ^ (tid & 7)) << 4) + 4 * k;
+#pragma unroll 1
                             for (uint32_t left = nan & 0x01010101u; left; left &= left - 1)
+#pragma unroll 1
                                 for (uint32_t seen = vis; seen; seen &= seen - 1) {
                                     const int d = d0 + ((__ffs(left) - 1) >> 3);
                                     atomicOr(&ms.nan[__ffs(seen) - 1][d >> 5], 1u << (d & 31));
@@ -505,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (tid == 0) part[RC * kD + r] = ms.m[r], part[RC * kD + RC + r] = sum;
                     continue;
                 }
-                const int rr = u.r0 + r, i = rr / G;
-                store_out(a, (int64_t)(u.row0 + i) * a.Hq + u.h * G + rr - i * G, tid, sum == 0.f ? 0.f : v / sum);
+                const int rr = u.r0 + r, i = (int)fdiv((uint32_t)rr, a.G);
+                store_out(a, (int64_t)(u.row0 + i) * a.Hq + walk.h * G + rr - i * G, tid, sum == 0.f ? 0.f : v / sum);
             }
             x += j1 - j0;
             if (x < end) walk.next();
@@ -527,9 +545,9 @@ cudaError_t launch_cols(const PagedAttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int ctas = 2 * device_sm_count();
     e = launch_smem_pdl(paged_cols_kernel<RC, QP, PP, QT>, ready, dim3(ctas), dim3(kThreads),
-                        Sh::kMisc + sizeof(Misc) + 1024, s, a, maps);
+                        Sh::kMisc + sizeof(Misc) + 1024, s, paged_lay_out(a, ctas), maps);
     if (e != cudaSuccess) return e;
-    return launch_paged_join<RC>(a, ctas, s);
+    return launch_paged_join<RC>(paged_lay_out(a, ctas), ctas, s);
 }
 
 // Rows of a unit: the least power of two that holds a sequence's rows of one
@@ -545,8 +563,10 @@ int unit_rows(int64_t pairs, bool f32) {
 size_t paged_attn_workspace(int64_t n_rows, int, int Hq, int Hkv, int64_t max_rows) {
     const int64_t rows = max_rows < n_rows ? max_rows : n_rows;
     const int rc = unit_rows(rows * (Hq / Hkv), false);
-    const size_t part = rc <= 8 ? part_stride<8>() : rc == 16 ? part_stride<16>() : part_stride<32>();
-    const size_t cols = (size_t)4 * device_sm_count() * part * sizeof(float);
+    const int ctas = 2 * device_sm_count();
+    const size_t cols = rc <= 8    ? paged_workspace<8>(ctas)
+                        : rc == 16 ? paged_workspace<16>(ctas)
+                                   : paged_workspace<32>(ctas);
     const size_t whole = paged_rows_workspace();
     return rows * (Hq / Hkv) > 32 && whole > cols ? whole : cols;
 }

@@ -18,11 +18,25 @@ size_t paged_rows_workspace();
 template <int RC>
 __host__ __device__ constexpr int64_t part_stride() { return RC * (kD + 2); }
 
+// Bytes of a workspace for `ctas` CTAs: a seam each, then two parts each.
+template <int RC>
+__host__ __device__ constexpr size_t paged_workspace(int ctas) {
+    return (size_t)ctas * 32 + (size_t)2 * ctas * part_stride<RC>() * sizeof(float);
+}
+// The arguments with the workspace laid out for `ctas` CTAs.
+inline PagedAttnArgs paged_lay_out(PagedAttnArgs a, int ctas) {
+    a.seams = static_cast<PagedSeam*>(a.workspace);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + (size_t)ctas * 32);
+    return a;
+}
+
 struct MapPair {
     CUtensorMap k, v;
 };
 
 #ifdef __CUDACC__
+
+static_assert(sizeof(PagedSeam) == 32, "seam layout");
 
 __device__ __forceinline__ void store_out(const PagedAttnArgs& a, int64_t row, int d, float v) {
     if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[row * kD + d] = __float2bfloat16_rn(v);
@@ -39,63 +53,77 @@ struct Waiter {
     }
 };
 
-constexpr int kJoinThreads = 128;  // one per channel
+constexpr int kJoinThreads = 128;
+constexpr int kMaxParts = 640;  // CTAs of the largest grid (two per SM of up to 320) and one more
 
-// Block (c, y), c < grid: if a unit crosses from CTA c - 1 into CTA c and began
-// in c - 1, joins its rows y, y + gridDim.y, ... Block (grid + b, y): zeros for
-// the rows of sequence b that lie in front of its first token.
+// Block (c, y), c < grid: where a unit crosses into CTA c and began in c - 1,
+// each warp joins one of its rows, lane = 4 channels. Block (grid + b, y):
+// zeros for the rows of sequence b that lie in front of its first token.
 template <int RC>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
+    __shared__ float factor[kJoinThreads / 32][kMaxParts];
+    const int lane = lane_id(), warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int d = threadIdx.x;
     if ((int)blockIdx.x >= grid) {
         const PagedSeq s = paged_seq(a.seqs, blockIdx.x - grid);
         const int64_t rows = s.rows < a.max_rows ? s.rows : a.max_rows;
         const int64_t blind = s.rows - s.len < rows ? s.rows - s.len : rows;
+#pragma unroll 1
         for (int64_t i = blockIdx.y; i < blind * a.Hq; i += gridDim.y)
-            store_out(a, (int64_t)s.row0 * a.Hq + i, d, 0.f);
+            store_out(a, (int64_t)s.row0 * a.Hq + i, threadIdx.x, 0.f);
         return;
     }
-    const int c = blockIdx.x;
-    PagedWalk<RC> walk(a);
-    const int64_t total = walk.total();
-    const int ctas = plan_ctas(total, grid);
-    if (c == 0 || c >= ctas) return;
-    const int64_t x = plan_begin(total, ctas, c);
-    const int j = walk.seek(x);
-    const PagedUnit u = walk.u;
-    const int64_t u0 = x - j, u1 = u0 + u.n;
-    if (j == 0 || u0 < plan_begin(total, ctas, c - 1)) return;
-    const int c1 = plan_cta(total, ctas, u1 - 1);
-    const int G = walk.G;
-    auto part = [&](int k) {
-        return a.part + (2 * k + (plan_begin(total, ctas, k) >= u0 ? 0 : 1)) * part_stride<RC>();
-    };
-    for (int r = blockIdx.y; r < u.rows; r += gridDim.y) {
-        float top = -INFINITY;
-        for (int k = c - 1; k <= c1; ++k) {
-            const float* p = part(k) + RC * kD + r;
-            if (p[RC] != 0.f) top = fmaxf(top, p[0]);
-        }
-        float sum = 0.f, acc = 0.f;
-        for (int k = c - 1; k <= c1; ++k) {
-            const float* p = part(k);
-            const float l = p[RC * kD + RC + r];
-            if (l == 0.f) continue;
-            const float f = exp2_approx(p[RC * kD + r] - top);
-            sum = fmaf(f, l, sum);
-            acc = fmaf(f, p[r * kD + d], acc);
-        }
-        const int rr = u.r0 + r, i = rr / G;
-        store_out(a, (int64_t)(u.row0 + i) * a.Hq + u.h * G + rr - i * G, d, sum == 0.f ? 0.f : acc / sum);
+    const PagedSeam seam = a.seams[blockIdx.x];
+    const int r = blockIdx.y * (kJoinThreads / 32) + warp;
+    if (!seam.live || r >= seam.rows) return;
+    const int c = blockIdx.x, n = seam.last - c + 2;
+    auto part = [&](int k) { return a.part + (k ? 2 * (c + k - 1) : seam.first) * part_stride<RC>(); };
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int k = lane; k < n; k += 32) {
+        const float* p = part(k) + RC * kD + r;
+        const float m = p[0], l = p[RC];
+        if (l != 0.f) top = fmaxf(top, m);
     }
+    top = warp_max(top);
+    float sum = 0.f;
+#pragma unroll 1
+    for (int k = lane; k < n; k += 32) {
+        const float* p = part(k) + RC * kD + r;
+        const float m = p[0], l = p[RC];
+        const float f = l != 0.f ? exp2_approx(m - top) : 0.f;
+        factor[warp][k] = f;
+        if (l != 0.f) sum = fmaf(f, l, sum);
+    }
+    sum = warp_sum(sum);
+    __syncwarp();
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(part(k) + r * kD + 4 * lane);
+        const float f = factor[warp][k];
+        const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (f != 0.f) acc[i] = fmaf(f, w[i], acc[i]);
+    }
+    const int rr = seam.r0 + r, i = (int)fdiv((uint32_t)rr, a.G), G = (int)a.G.d;
+    const int64_t at = ((int64_t)(seam.row0 + i) * a.Hq + seam.h * G + rr - i * G) * kD + 4 * lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = sum == 0.f ? 0.f : acc[k] / sum;
+    if (a.out_bf16)
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at) =
+            make_uint2((uint32_t)f32_to_bf16_rn(acc[0]) | ((uint32_t)f32_to_bf16_rn(acc[1]) << 16),
+                       (uint32_t)f32_to_bf16_rn(acc[2]) | ((uint32_t)f32_to_bf16_rn(acc[3]) << 16));
+    else
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(acc[0], acc[1], acc[2], acc[3]);
 }
 
 template <int RC>
 cudaError_t launch_paged_join(const PagedAttnArgs& a, int grid, cudaStream_t s) {
     static std::atomic<unsigned long long> ready{0};
-    return launch_smem_pdl(paged_join_kernel<RC>, ready, dim3(grid + a.seqs.B, RC < 32 ? RC : 32),
-                           dim3(kJoinThreads), 0, s, a, grid);
+    return launch_smem_pdl(paged_join_kernel<RC>, ready, dim3(grid + a.seqs.B, RC / 4), dim3(kJoinThreads), 0, s, a,
+                           grid);
 }
 
 #endif  // __CUDACC__

@@ -3,9 +3,9 @@
 // the 128-token tiles that some row of it sees. The units' tiles, laid end to
 // end (sequence, kv-head, group), are cut into equal ranges, one per CTA: no
 // CTA waits for a longer one, whatever the lengths, and a long context is
-// split by itself. A unit inside one range is finished by its CTA; pieces of
-// a unit that spans ranges are joined by a second kernel. Lengths are on the
-// device, so every warp derives its range itself.
+// split by itself. A unit inside one range is finished by its CTA; parts of
+// a unit that spans ranges go to the workspace and are joined by a second
+// kernel. Lengths are on the device, so a warp of each CTA derives its range.
 #pragma once
 
 #include "paged.cuh"
@@ -19,143 +19,71 @@ constexpr int kTile = 128;  // tokens per tile
 // What the rows of a unit see. Row r of the unit is row r0 + r of the
 // sequence's rows x G (head fastest).
 struct PagedUnit {
-    int b, h, g;
     int row0;        // first packed row of the sequence
     int first_pos;   // position of the sequence's row 0 (may be negative)
     int rows;        // (query row, head) pairs of the unit
     int r0;
     int p0, p1;      // least and largest position
     int lo_tok;      // first token of p0's window
-    int lo, hi;      // tiles of the windows: [lo, hi)
-    int sink_tiles;  // tiles of the sinks in front of them
+    int lo;          // tiles: `sink_tiles` of the sinks, then those from lo on
+    int sink_tiles;
     int n;           // tiles in all
     __device__ __forceinline__ int tile(int j) const { return j < sink_tiles ? j : j - sink_tiles + lo; }
 };
 
+// Where a CTA's range begins and ends, and the unit it begins in.
+struct PagedRange {
+    int64_t begin, end;
+    int b, h, g, j0;  // j0: first tile of the range in its unit
+};
+
+// A unit that crosses from CTA c - 1 into CTA c and began in c - 1 (kept by c):
+// its parts are slot `first`, then 2k of CTAs k = c .. last.
+struct PagedSeam {
+    int live, first, last;
+    int row0, r0, rows, h;
+    int pad;
+};
+
+template <int RC>
+__device__ __forceinline__ int paged_groups(const PagedAttnArgs& a, const PagedSeq& q) {
+    const int r = q.rows < a.max_rows ? q.rows : (int)a.max_rows;
+    return (int)((r * (int64_t)a.G.d + RC - 1) / RC);
+}
+
+template <int RC>
+__device__ __forceinline__ PagedUnit paged_unit(const PagedAttnArgs& a, const PagedSeq& q, int g) {
+    PagedUnit v;
+    const int G = (int)a.G.d;
+    const int r = q.rows < a.max_rows ? q.rows : (int)a.max_rows;
+    v.r0 = g * RC;  // n_rows * Hq < 2^31
+    v.rows = r * G - v.r0 < RC ? r * G - v.r0 : RC;
+    v.row0 = q.row0;
+    v.first_pos = q.len - q.rows;
+    v.p0 = v.first_pos + (int)fdiv((uint32_t)v.r0, a.G);
+    v.p1 = v.first_pos + (int)fdiv((uint32_t)(v.r0 + v.rows - 1), a.G);
+    const int hi = v.p1 >= 0 && q.len > 0 ? v.p1 / kTile + 1 : 0;
+    v.lo_tok = a.window && v.p0 >= a.window ? v.p0 - a.window + 1 : 0;
+    v.lo = v.lo_tok / kTile;
+    const int st = a.sinks / kTile + (a.sinks % kTile != 0);
+    v.sink_tiles = st < v.lo ? st : v.lo;
+    v.n = hi > v.lo ? v.sink_tiles + hi - v.lo : 0;
+    return v;
+}
+
+// The units of a CTA's range, one after the other.
 template <int RC>
 struct PagedWalk {
     const PagedAttnArgs& a;
     PagedSeq s;
-    int G, b = 0, h = 0, g = 0, groups = 0;
-    int64_t first_chunk = 0;  // this lane's sequence of the first 32: its tiles for one kv-head
+    int b, h, g, groups;
     PagedUnit u;
 
-    __device__ __forceinline__ explicit PagedWalk(const PagedAttnArgs& args) : a(args), G(args.Hq / args.Hkv) {}
-
-    __device__ __forceinline__ int group_count(const PagedSeq& q) const {
-        const int64_t r = q.rows < a.max_rows ? q.rows : a.max_rows;
-        return (int)((r * G + RC - 1) / RC);
-    }
-    __device__ __forceinline__ PagedUnit unit(const PagedSeq& q, int gi) const {
-        PagedUnit v;
-        const int64_t all = (q.rows < a.max_rows ? q.rows : a.max_rows) * (int64_t)G;
-        v.r0 = gi * RC;
-        v.rows = (int)(all - v.r0 < RC ? all - v.r0 : RC);
-        v.row0 = q.row0;
-        v.first_pos = q.len - q.rows;
-        v.p0 = v.first_pos + v.r0 / G;
-        v.p1 = v.first_pos + (v.r0 + v.rows - 1) / G;
-        v.hi = v.p1 >= 0 && q.len > 0 ? v.p1 / kTile + 1 : 0;
-        v.lo_tok = a.window && v.p0 >= a.window ? v.p0 - a.window + 1 : 0;
-        v.lo = v.lo_tok / kTile;
-        const int st = a.sinks / kTile + (a.sinks % kTile != 0);
-        v.sink_tiles = st < v.lo ? st : v.lo;
-        v.n = v.hi > v.lo ? v.sink_tiles + v.hi - v.lo : 0;
-        v.b = b;
-        v.h = h;
-        v.g = gi;
-        return v;
-    }
-    // This lane's sequence of chunk b0 .. b0 + 31: the tiles of its units for one
-    // kv-head. Every lane of the warp calls it together. Sequences of a few
-    // groups are summed by their lane, longer ones by the warp (a prompt has
-    // tens of groups and may be the only sequence).
-    __device__ __forceinline__ int64_t head_tiles(int b0) const {
-        constexpr int kFew = 2;
-        const int lane = lane_id();
-        PagedSeq q{};
-        int n = 0;
-        if (b0 + lane < a.seqs.B) {
-            q = paged_seq(a.seqs, b0 + lane);
-            n = group_count(q);
-        }
-        int64_t t = 0;
-        if (n <= kFew)
-            for (int i = 0; i < n; ++i) t += unit(q, i).n;
-        for (unsigned many = __ballot_sync(kFull, n > kFew); many; many &= many - 1) {
-            const int src = __ffs(many) - 1;
-            PagedSeq o;
-            o.row0 = 0;
-            o.rows = __shfl_sync(kFull, q.rows, src);
-            o.len = __shfl_sync(kFull, q.len, src);
-            const int m = __shfl_sync(kFull, n, src);
-            int64_t part = 0;
-            for (int i = lane; i < m; i += 32) part += unit(o, i).n;
-#pragma unroll
-            for (int k = 16; k; k >>= 1) part += __shfl_xor_sync(kFull, part, k);
-            if (lane == src) t = part;
-        }
-        return t;
-    }
-    // Tiles of all sequences. Every lane of the warp calls it together.
-    __device__ __forceinline__ int64_t total() {
-        int64_t t = 0;
-        for (int b0 = 0; b0 < a.seqs.B; b0 += 32) {
-            const int64_t mine = head_tiles(b0);
-            if (b0 == 0) first_chunk = mine;
-            t += mine;
-        }
-#pragma unroll
-        for (int m = 16; m; m >>= 1) t += __shfl_xor_sync(kFull, t, m);
-        return t * a.Hkv;
-    }
-    // Goes to the unit that holds tile x < total(), which was called before;
-    // returns the tile's number in it. Every lane of the warp calls it together.
-    __device__ __forceinline__ int seek(int64_t x) {
-        const int lane = lane_id();
-        int64_t before = 0, per_head = 1;
-        b = 0;
-        for (int b0 = 0; b0 < a.seqs.B; b0 += 32) {
-            const int64_t mine = b0 ? head_tiles(b0) : first_chunk;
-            int64_t incl = mine * a.Hkv;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const int64_t o = __shfl_up_sync(kFull, incl, m);
-                if (lane >= m) incl += o;
-            }
-            const unsigned hit = __ballot_sync(kFull, x < before + incl);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                b = b0 + src;
-                per_head = __shfl_sync(kFull, mine, src);
-                x -= before + __shfl_sync(kFull, incl, src) - per_head * a.Hkv;
-                break;
-            }
-            before += __shfl_sync(kFull, incl, 31);
-        }
+    __device__ __forceinline__ PagedWalk(const PagedAttnArgs& args, const PagedRange& r)
+        : a(args), b(r.b), h(r.h), g(r.g) {
         s = paged_seq(a.seqs, b);
-        groups = group_count(s);
-        h = (int)(x / per_head);
-        x -= h * per_head;
-        for (int g0 = 0; g0 < groups; g0 += 32) {
-            const int mine = g0 + lane < groups ? unit(s, g0 + lane).n : 0;
-            int64_t incl = mine;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const int64_t o = __shfl_up_sync(kFull, incl, m);
-                if (lane >= m) incl += o;
-            }
-            const unsigned hit = __ballot_sync(kFull, x < incl);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                g = g0 + src;
-                x -= __shfl_sync(kFull, incl, src) - __shfl_sync(kFull, mine, src);
-                break;
-            }
-            x -= __shfl_sync(kFull, incl, 31);
-        }
-        u = unit(s, g);
-        return (int)x;
+        groups = paged_groups<RC>(a, s);
+        u = paged_unit<RC>(a, s, g);
     }
     // The next unit that has tiles; past the last one, u.n = 0.
     __device__ __forceinline__ void next() {
@@ -170,20 +98,134 @@ struct PagedWalk {
                             return;
                         }
                         s = paged_seq(a.seqs, b);
-                        groups = group_count(s);
+                        groups = paged_groups<RC>(a, s);
                     } while (groups == 0);
                 }
             }
-            u = unit(s, g);
+            u = paged_unit<RC>(a, s, g);
         } while (u.n == 0);
     }
 };
 
-// CTA c of n = plan_ctas takes tiles [plan_begin(c), plan_begin(c + 1)) of
-// total, at least one; tile x belongs to CTA plan_cta(x).
-__device__ __forceinline__ int plan_ctas(int64_t total, int grid) { return total < grid ? (int)total : grid; }
-__device__ __forceinline__ int64_t plan_begin(int64_t total, int n, int c) { return total * c / n; }
-__device__ __forceinline__ int plan_cta(int64_t total, int n, int64_t x) { return (int)(((x + 1) * n - 1) / total); }
+// The tiles of this lane's sequence of chunk b0 .. b0 + 31, for one kv-head.
+// Every lane of the warp calls it together. Sequences of a few groups are
+// summed by their lane, longer ones by the warp (a prompt has tens of groups
+// and may be the only sequence).
+template <int RC>
+__device__ __noinline__ int64_t paged_head_tiles(const PagedAttnArgs& a, int b0) {
+    constexpr int kFew = 2;
+    const int lane = lane_id();
+    PagedSeq q{};
+    int n = 0;
+    if (b0 + lane < a.seqs.B) {
+        q = paged_seq(a.seqs, b0 + lane);
+        n = paged_groups<RC>(a, q);
+    }
+    int64_t t = 0;
+#pragma unroll 1
+    for (int i = 0; i < n && n <= kFew; ++i) t += paged_unit<RC>(a, q, i).n;
+#pragma unroll 1
+    for (unsigned many = __ballot_sync(kFull, n > kFew); many; many &= many - 1) {
+        const int src = __ffs(many) - 1;
+        PagedSeq o{};
+        o.rows = __shfl_sync(kFull, q.rows, src);
+        o.len = __shfl_sync(kFull, q.len, src);
+        const int m = __shfl_sync(kFull, n, src);
+        int64_t part = 0;
+#pragma unroll 1
+        for (int i = lane; i < m; i += 32) part += paged_unit<RC>(a, o, i).n;
+#pragma unroll
+        for (int k = 16; k; k >>= 1) part += __shfl_xor_sync(kFull, part, k);
+        if (lane == src) t = part;
+    }
+    return t;
+}
+
+__device__ __forceinline__ int64_t warp_prefix(int64_t v) {  // inclusive
+    const int lane = lane_id();
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t o = __shfl_up_sync(kFull, v, m);
+        if (lane >= m) v += o;
+    }
+    return v;
+}
+
+// The range of CTA c of `grid`, and the seam in front of it. With fewer tiles
+// than CTAs, the first `total` take one each. Every lane of one warp calls it
+// together; all get the result.
+template <int RC>
+__device__ __noinline__ PagedRange paged_plan(const PagedAttnArgs& a, int grid, int c) {
+    const int lane = lane_id();
+    PagedRange r{};
+    int64_t total = 0, first_chunk = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.seqs.B; b0 += 32) {
+        const int64_t mine = paged_head_tiles<RC>(a, b0);
+        if (b0 == 0) first_chunk = mine;
+        total += mine;
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
+    total *= a.Hkv;
+    const int n = total < grid ? (int)total : grid;
+    // CTA k takes tiles [total * k / n, total * (k + 1) / n)
+    int64_t edge = 0;  // lanes 0-2: edges c - 1, c, c + 1
+    if (c < n && lane < 3 && c + lane > 0) edge = total * (c + lane - 1) / n;
+    const int64_t prev = __shfl_sync(kFull, edge, 0);
+    r.begin = __shfl_sync(kFull, edge, 1);
+    r.end = __shfl_sync(kFull, edge, 2);
+    PagedSeam seam{};
+    if (c < n) {
+        int64_t x = r.begin, before = 0, per_head = 1;
+#pragma unroll 1
+        for (int b0 = 0; b0 < a.seqs.B; b0 += 32) {
+            const int64_t mine = b0 ? paged_head_tiles<RC>(a, b0) : first_chunk;
+            const int64_t incl = warp_prefix(mine * a.Hkv);
+            const unsigned hit = __ballot_sync(kFull, x < before + incl);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                r.b = b0 + src;
+                per_head = __shfl_sync(kFull, mine, src);
+                x -= before + __shfl_sync(kFull, incl, src) - per_head * a.Hkv;
+                break;
+            }
+            before += __shfl_sync(kFull, incl, 31);
+        }
+        const PagedSeq s = paged_seq(a.seqs, r.b);
+        const int groups = paged_groups<RC>(a, s);
+        r.h = (int)(x / per_head);
+        x -= r.h * per_head;
+#pragma unroll 1
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int64_t mine = g0 + lane < groups ? paged_unit<RC>(a, s, g0 + lane).n : 0;
+            const int64_t incl = warp_prefix(mine);
+            const unsigned hit = __ballot_sync(kFull, x < incl);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                r.g = g0 + src;
+                x -= __shfl_sync(kFull, incl - mine, src);
+                break;
+            }
+            x -= __shfl_sync(kFull, incl, 31);
+        }
+        r.j0 = (int)x;
+        const PagedUnit u = paged_unit<RC>(a, s, r.g);
+        const int64_t u0 = r.begin - r.j0;
+        if (c > 0 && r.j0 > 0 && u0 >= prev) {
+            seam.live = 1;
+            seam.first = 2 * (c - 1) + (u0 > prev ? 1 : 0);
+            // the CTA of the unit's last tile x: the last k with edge(k) <= x
+            seam.last = (int)(((u0 + u.n) * n - 1) / total);
+            seam.row0 = u.row0;
+            seam.r0 = u.r0;
+            seam.rows = u.rows;
+            seam.h = r.h;
+        }
+    }
+    if (lane == 0) a.seams[c] = seam;
+    return r;
+}
 
 #endif  // __CUDACC__
 

@@ -50,6 +50,7 @@ struct Misc {
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2], w_full[2], w_free[2], sc_full[kRing];
     uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem;
+    PagedRange range;
     uint32_t ok[kRing];                // pages of the tile that were loaded
     float2 scale[kRing][kMaxSlots];    // (k scale, v scale) of a page
     uint32_t nan[RC][4];               // row: channels that a NaN code of a partly seen tile reaches
@@ -85,6 +86,7 @@ __device__ __forceinline__ float write_row(const PagedAttnArgs& a, const __nv_bf
     e = bad ? 0 : (e < -126 ? -126 : e);
     float up = __uint_as_float((uint32_t)(127 - e) << 23);
     if (a.scale_log2 < 0.f) up = -up;
+#pragma unroll 1
     for (int c = 0; c < 8; ++c) {
         uint32_t h[4] = {0, 0, 0, 0}, l[4] = {0, 0, 0, 0};
         if (real) {
@@ -123,57 +125,124 @@ struct View {
     }
 };
 
-// Weights of a row over a tile, packed in fp16 pairs; `most` is the largest
-// exponent met (bias in), `sum` the sum of p.
-template <bool MASKED>
-__device__ __forceinline__ void row_weights(uint32_t s, const float2* scale, int page_log, float c, float m, float rv,
-                                            const View& view, uint32_t (&p)[64], float& most, float& sum) {
-    uint64_t acc = pk2(0.f, 0.f);
-    most = -INFINITY;
-    const uint64_t nm = pk2(kBias - m, kBias - m);
+// A row's running state in a segment.
+struct RowState {
+    float c;           // score scale (softmax scale, log2 e, query scale)
+    float m, l;        // running maximum (log2 units), sum of 2^(s - m + kBias)
+    float vref, rv;    // largest v scale so far and its reciprocal
+};
+
+// Multiplies a row's weights of the tile so far (`done` columns of fp16 pairs)
+// and, behind the first tile, its output by a factor.
+__device__ __noinline__ void rescale_row(uint32_t s, int done, uint32_t o, bool have_o, float fp, float fo) {
+    const uint32_t f2 = f16x2(fp, fp);
+#pragma unroll 1
+    for (int i = 0; i < done; i += 8) {
+        float v[8];
+        tmem_ld<8>(s + i, v);
 #pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t h = __float_as_uint(v[k]);
+            asm("mul.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(f2));
+            v[k] = __uint_as_float(h);
+        }
+        tmem_st8(s + i, v);
+    }
+#pragma unroll 1
+    for (int i = 0; have_o && i < kD; i += 8) {
+        float v[8];
+        tmem_ld<8>(o + i, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= fo;
+        tmem_st8(o + i, v);
+    }
+    tmem_wait_st();
+}
+
+// The weights of a row over a tile, 32 columns at a time, in fp16 pairs over
+// the front of its scores: column pair i of P takes the place of score i,
+// which has been read by then. Where a chunk's largest exponent passes the
+// lag, the warp raises its rows' maxima to that chunk's.
+template <bool MASKED>
+__device__ __forceinline__ void row_tile(uint32_t s, uint32_t o, bool have_o, const float2* scale, int page_log,
+                                         bool real, const View& view, RowState& st) {
+#pragma unroll 1
     for (int q = 0; q < 4; ++q) {
-        float v[32];
-        tmem_ld<32>(s + 32 * q, v);
         const uint32_t seen = MASKED ? view.bits(32 * q) : kFull;
+        float v[32], most;
+        float2 kv[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) kv[g] = scale[(32 * q + 16 * g) >> page_log];
+        auto exponents = [&]() {
+            tmem_ld<32>(s + 32 * q, v);
+            const uint64_t nm = pk2(kBias - st.m, kBias - st.m);
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const float f = kv[g].x * st.c;
+                const uint64_t f2 = pk2(f, f);
+#pragma unroll
+                for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                    float2 x = upk2(fma2(pk2(v[i], v[i + 1]), f2, nm));
+                    if (MASKED) {
+                        x.x = (seen >> i) & 1u ? x.x : -INFINITY;
+                        x.y = (seen >> i) & 2u ? x.y : -INFINITY;
+                    }
+                    v[i] = x.x;
+                    v[i + 1] = x.y;
+                    top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(x.x, x.y));
+                }
+            }
+            most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        };
+        exponents();
+        if (__any_sync(kFull, real && most > kBias + kLag)) {
+            // scores again, without the maximum (it may be -inf still)
+            const float m = st.m;
+            st.m = 0.f;
+            exponents();
+            most -= kBias;
+            const float mn = real ? fmaxf(m, most) : 0.f;
+            const float f = m == mn ? 1.f : exp2_approx(m - mn);
+            st.m = mn;
+            st.l *= f;
+            rescale_row(s, 16 * q, o, have_o, f, f);
+            exponents();
+        }
+        uint64_t acc0 = pk2(0.f, 0.f), acc1 = acc0;
+        uint32_t p[16];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            const float2 kv = scale[(32 * q + 16 * g) >> page_log];
-            const float f = kv.x * c, w = kv.y * rv;
-            const uint64_t f2 = pk2(f, f), w2 = pk2(w, w);
+            const float w = kv[g].y * st.rv;
             const bool weigh = w != 1.f;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const int at = 16 * g + i;
-                float2 x = upk2(fma2(pk2(v[at], v[at + 1]), f2, nm));
-                if (MASKED) {
-                    x.x = (seen >> at) & 1u ? x.x : -INFINITY;
-                    x.y = (seen >> at) & 2u ? x.y : -INFINITY;
-                }
-                most = fmaxf(most, fmaxf(x.x, x.y));
-                v[at] = exp2_approx(x.x);
-                v[at + 1] = exp2_approx(x.y);
-                acc = add2(acc, pk2(v[at], v[at + 1]));
+            for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                v[i] = exp2_approx(v[i]);
+                v[i + 1] = exp2_approx(v[i + 1]);
+                if (i & 2) acc1 = add2(acc1, pk2(v[i], v[i + 1]));
+                else acc0 = add2(acc0, pk2(v[i], v[i + 1]));
             }
             if (weigh) {
+                const uint64_t w2 = pk2(w, w);
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const int at = 16 * g + i;
-                    float2 y = upk2(mul2(pk2(v[at], v[at + 1]), w2));
+                for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                    float2 y = upk2(mul2(pk2(v[i], v[i + 1]), w2));
                     if (MASKED) {  // the scale of a page that was not loaded is void
-                        y.x = (seen >> at) & 1u ? y.x : 0.f;
-                        y.y = (seen >> at) & 2u ? y.y : 0.f;
+                        y.x = (seen >> i) & 1u ? y.x : 0.f;
+                        y.y = (seen >> i) & 2u ? y.y : 0.f;
                     }
-                    v[at] = y.x;
-                    v[at + 1] = y.y;
+                    v[i] = y.x;
+                    v[i + 1] = y.y;
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) p[(32 * q + 16 * g + i) / 2] = f16x2(v[16 * g + i], v[16 * g + i + 1]);
+            for (int i = 16 * g; i < 16 * g + 16; i += 2) p[i / 2] = f16x2(v[i], v[i + 1]);
         }
+        const float2 t = upk2(add2(acc0, acc1));
+        st.l += t.x + t.y;
+        tmem_st16(s + 16 * q, p);
     }
-    const float2 t = upk2(acc);
-    sum = t.x + t.y;
+    tmem_wait_st();
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -210,31 +279,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    PagedWalk<RC> walk(a);
-    const int64_t total = walk.total();
-    const int ctas = plan_ctas(total, gridDim.x);
-    const bool used = (int)blockIdx.x < ctas;
-    const int64_t begin = used ? plan_begin(total, ctas, blockIdx.x) : 0;
-    const int64_t end = used ? plan_begin(total, ctas, blockIdx.x + 1) : 0;
-    const int G = a.Hq / a.Hkv, slots = kTile / a.page, page_log = 31 - __clz(a.page);
+    if (warp == 0) {
+        const PagedRange r = paged_plan<RC>(a, gridDim.x, blockIdx.x);
+        if (lane == 0) ms.range = r;
+    }
+    __syncthreads();
+    const int64_t begin = ms.range.begin, end = ms.range.end;
+    int j0 = ms.range.j0;  // first tile of the segment in its unit
+    PagedWalk<RC> walk(a, ms.range);
+    if (begin >= end) walk.u.n = 0;
+    const int G = (int)a.G.d, slots = kTile / a.page, page_log = 31 - __clz(a.page);
     if (blockIdx.x == 0 && warp == 12 && a.seqs.status)
+#pragma unroll 1
         for (int i = lane; i < a.seqs.B; i += 32) {
             const PagedSeq q = paged_seq(a.seqs, i);
             paged_report(a.seqs, q.bad | (q.rows > a.max_rows ? kBadLength : 0u));
         }
     Waiter wait;
-    int j0 = begin < end ? walk.seek(begin) : 0;  // first tile of the segment in its unit
-    uint32_t it = 0;                              // tiles of this CTA so far
+    uint32_t it = 0;  // tiles of this CTA so far
 
     if (warp >= 12) {
         regs_dec<kIssueRegs>();
         if (warp == 12) {
         // ------------------------------------------------------------ TMA --
         bool missing = false;
+#pragma unroll 1
         for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
             const PagedUnit u = walk.u;
             const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
-            const int32_t* row = a.seqs.table + u.b * a.seqs.table_stride;
+            const int32_t* row = a.seqs.table + walk.b * a.seqs.table_stride;
             auto fetch = [&](int j) -> int {  // this lane's page of a tile, -1 where no row sees it
                 if (lane >= slots || j >= j1) return -1;
                 const int slot = u.tile(j) * slots + lane, t0 = slot << page_log;
@@ -245,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return -1;
             };
             int id = fetch(j0);
+#pragma unroll 1
             for (int j = j0; j < j1; ++j, ++it) {
                 const int next = fetch(j + 1);
                 const uint32_t ks = it % kKStages, vs = it & 1, ring = it % kRing;
@@ -252,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const unsigned have = __ballot_sync(kFull, id >= 0);
                 const uint32_t bytes = (uint32_t)__popc(have) * (uint32_t)a.page * 128u;
                 const uint32_t off = (uint32_t)lane * (uint32_t)a.page * 128u;
-                const int tile = id * a.Hkv + u.h;
+                const int tile = id * a.Hkv + walk.h;
                 wait(smem_u32(&ms.k_empty[ks]), ((it / kKStages) & 1) ^ 1);
                 if (lane == 0) {
                     mbar_arrive_tx(k_full, bytes);
@@ -276,20 +350,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x < end) walk.next();
         }
         if (missing) paged_report(a.seqs, kBadPage);
+#pragma unroll 1
         for (uint32_t i = it < 3 ? 0 : it - 3; i < it; ++i)  // no copy is in flight at the end
             wait(smem_u32(&ms.k_full[i % kKStages]), (i / kKStages) & 1);
+#pragma unroll 1
         for (uint32_t i = it < 2 ? 0 : it - 2; i < it; ++i) wait(smem_u32(&ms.v_full[i & 1]), (i >> 1) & 1);
         } else if (warp == 13) {
         // ------------------------------------------------------------ MMA --
         if (lane == 0) {
             constexpr uint32_t id_s = mma_idesc(128, 128, false, false), id_o = mma_idesc(128, 128, false, true);
             uint32_t seg[2] = {0, 0}, np[2] = {0, 0};  // segments and weight tiles of each half
+#pragma unroll 1
             for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
                 const int cnt = end - x < walk.u.n - j0 ? (int)(end - x) : walk.u.n - j0;
                 const int halves = walk.u.rows > 128 ? 2 : 1;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)
                     if (hf < halves) wait(smem_u32(&ms.q_ready[hf]), seg[hf]++ & 1);
+#pragma unroll 1
                 for (int i = 0; i <= cnt; ++i) {
                     const uint32_t t = it + i, tp = t - 1;
 #pragma unroll
@@ -334,11 +412,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<kValueRegs>();
         const int tok = tid - 256;  // token of the tile
         uint32_t seg[2] = {0, 0};
+#pragma unroll 1
         for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
             const PagedUnit u = walk.u;
             const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
             wait(smem_u32(&ms.q_ready[0]), seg[0]++ & 1);  // the rows' NaN marks are clear
             if (u.rows > 128) wait(smem_u32(&ms.q_ready[1]), seg[1]++ & 1);
+#pragma unroll 1
             for (int j = j0; j < j1; ++j, ++it) {
                 const uint32_t buf = it & 1, ring = it % kRing;
                 wait(smem_u32(&ms.sc_full[ring]), (it / kRing) & 1);
@@ -351,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool all = have && t <= u.p0 && (!a.window || sink || t > u.p1 - a.window);
                 const uint8_t* src = sm + kV + buf * 16384 + tok * 128;
                 uint8_t* dst = sm + kV16 + buf * 32768 + tok * 128;
-#pragma unroll
+#pragma unroll 2
                 for (int c = 0; c < 8; ++c) {  // 16 channels each
                     uint4 q = *reinterpret_cast<const uint4*>(src + ((c ^ (tok & 7)) << 4));
                     uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -361,8 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!some) w[k] = 0;
                             const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
                             w[k] &= ~nan;
+#pragma unroll 1
                             for (uint32_t left = nan & 0x01010101u; left; left &= left - 1) {
                                 const int d = 16 * c + 4 * k + ((__ffs(left) - 1) >> 3);
+#pragma unroll 1
                                 for (int r = 0; r < u.rows; ++r) {
                                     const int gap = u.first_pos + (u.r0 + r) / G - t;
                                     if (gap >= 0 && (!a.window || sink || gap < a.window))
@@ -396,27 +478,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_at = tmem + lanes + hf * 128, o_at = tmem + lanes + 256 + hf * 128;
         const uint32_t all_slots = (1u << slots) - 1u;
         uint32_t n = 0, seg = 0;  // weight tiles and segments of this half
+#pragma unroll 1
         for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
             const PagedUnit u = walk.u;
             const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
             if (hf * 128 < u.rows) {
                 const bool real = r < u.rows;
-                const int rr = u.r0 + (real ? r : 0), qi = rr / G;
-                const int64_t out_row = (int64_t)(u.row0 + qi) * a.Hq + u.h * G + rr - qi * G;
+                const int rr = u.r0 + (real ? r : 0), qi = (int)fdiv((uint32_t)rr, a.G);
+                const int64_t out_row = (int64_t)(u.row0 + qi) * a.Hq + walk.h * G + rr - qi * G;
                 const int pos = real ? u.first_pos + qi : -1;
                 // least and largest position of the warp's rows
                 const int w0 = u.r0 + 32 * warp;
                 const int wn = u.rows - 32 * warp < 32 ? u.rows - 32 * warp : 32;
-                const int wp0 = u.first_pos + w0 / G, wp1 = u.first_pos + (w0 + (wn > 0 ? wn : 1) - 1) / G;
+                const int wp0 = u.first_pos + (int)fdiv((uint32_t)w0, a.G);
+                const int wp1 = u.first_pos + (int)fdiv((uint32_t)(w0 + (wn > 0 ? wn : 1) - 1), a.G);
                 const float c = write_row(a, reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                 (int64_t)(u.row0 + qi) * a.q_st + (int64_t)(u.h * G + rr - qi * G) * a.q_sh,
+                                                 (int64_t)(u.row0 + qi) * a.q_st + (int64_t)(walk.h * G + rr - qi * G) * a.q_sh,
                                           real, sm + kQ + hf * 32768, lrow);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) ms.nan[r][k] = 0u;
                 proxy_fence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready[hf]));
-                float m = real ? -INFINITY : 0.f, l = 0.f, vref = 0.f, rv = 0.f;
+                RowState st{c, real ? -INFINITY : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
                 for (int j = j0; j < j1; ++j, ++it, ++n) {
                     const uint32_t ring = it % kRing;
                     wait(smem_u32(&ms.s_full[hf]), n & 1);
@@ -429,53 +514,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        (!a.window || t0 > wp1 - a.window || t0 + kTile <= a.sinks);
                     const View view{pos - t0, a.window ? pos - t0 - a.window : -1, a.sinks - t0, ok, page_log};
                     float vmax = 0.f;
+#pragma unroll 1
                     for (int i = 0; i < slots; ++i)
                         if ((ok >> i) & 1u) vmax = fmaxf(vmax, scale[i].y);
-                    uint32_t p[64];
-                    float most, sum;
-#pragma unroll 1
-                    for (bool raised = false;; raised = true) {
-                        if (whole) row_weights<false>(s_at, scale, page_log, c, m, rv, view, p, most, sum);
-                        else row_weights<true>(s_at, scale, page_log, c, m, rv, view, p, most, sum);
-                        if (raised || !__any_sync(kFull, (real && most > kBias + kLag) || vmax > vref)) break;
-                        // raise the maxima and the v scale of the warp's rows
-                        float top = -INFINITY;
-#pragma unroll 1
-                        for (int q = 0; q < 4; ++q) {
-                            float v[32];
-                            tmem_ld<32>(s_at + 32 * q, v);
-                            const uint32_t seen = view.bits(32 * q);
-#pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                const float f = scale[(32 * q + 16 * g) >> page_log].x * c;
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if ((seen >> (16 * g + i)) & 1u) top = fmaxf(top, v[16 * g + i] * f);
-                            }
-                        }
-                        const float mn = real ? fmaxf(m, top) : 0.f, vn = fmaxf(vref, vmax);
-                        const float f = m == mn ? 1.f : exp2_approx(m - mn);
-                        const float fo = vref > 0.f ? f * (vref / vn) : 0.f;
-                        m = mn;
-                        l *= f;
-                        vref = vn;
-                        rv = vn > 0.f ? 1.f / vn : 0.f;
-                        if (j > j0) {  // P V of the tile before is complete: S came after it
-#pragma unroll 1
-                            for (int q = 0; q < 4; ++q) {
-                                float v[32];
-                                uint32_t w[32];
-                                tmem_ld<32>(o_at + 32 * q, v);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i] * fo);
-                                tmem_st32(o_at + 32 * q, w);
-                            }
-                        }
+                    // O is quiet: P V of the tile before came in front of this S
+                    if (vmax > st.vref) {
+                        rescale_row(s_at, 0, o_at, j > j0, 1.f, st.vref / vmax);
+                        st.vref = vmax;
+                        st.rv = 1.f / vmax;
                     }
-                    l += sum;
-                    tmem_st32(s_at, p);
-                    tmem_st32(s_at + 32, p + 32);
-                    tmem_wait_st();
+                    if (whole) row_tile<false>(s_at, o_at, j > j0, scale, page_log, real, view, st);
+                    else row_tile<true>(s_at, o_at, j > j0, scale, page_log, real, view, st);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&ms.p_full[hf]));
@@ -484,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const bool complete = j0 == 0 && j1 == u.n;
                 float* part = a.part + (2 * blockIdx.x + (x == begin ? 0 : 1)) * part_stride<RC>();
-                const float inv = complete ? (l == 0.f ? 0.f : vref / l) : vref;
+                const float inv = complete ? (st.l == 0.f ? 0.f : st.vref / st.l) : st.vref;
                 __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + out_row * kD;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
@@ -509,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<float4*>(part + r * kD + 32 * q + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
-                if (!complete && real) part[RC * kD + r] = m, part[RC * kD + RC + r] = l;
+                if (!complete && real) part[RC * kD + r] = st.m, part[RC * kD + RC + r] = st.l;
                 tc_fence_before();
             } else {
                 it += j1 - j0;
@@ -525,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-size_t paged_rows_workspace() { return (size_t)2 * device_sm_count() * part_stride<RC>() * sizeof(float); }
+size_t paged_rows_workspace() { return paged_workspace<RC>(device_sm_count()); }
 
 cudaError_t launch_paged_rows(const PagedAttnArgs& a, cudaStream_t s) {
     static std::atomic<unsigned long long> ready{0};
@@ -534,9 +583,9 @@ cudaError_t launch_paged_rows(const PagedAttnArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = make_pool_map(&maps.v, a.vc, a.num_pages * a.Hkv, a.page);
     if (e != cudaSuccess) return e;
     const int ctas = device_sm_count();
-    e = launch_smem_pdl(paged_rows_kernel, ready, dim3(ctas), dim3(kThreads), kMisc + sizeof(Misc) + 1024, s, a, maps);
+    e = launch_smem_pdl(paged_rows_kernel, ready, dim3(ctas), dim3(kThreads), kMisc + sizeof(Misc) + 1024, s, paged_lay_out(a, ctas), maps);
     if (e != cudaSuccess) return e;
-    return launch_paged_join<RC>(a, ctas, s);
+    return launch_paged_join<RC>(paged_lay_out(a, ctas), ctas, s);
 }
 
 }  // namespace nsnq
