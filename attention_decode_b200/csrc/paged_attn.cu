@@ -35,6 +35,7 @@ namespace {
 constexpr int kThreads = 192;  // warps 0-3: tokens / channels; 4: TMA; 5: MMA issue
 constexpr float kLag = 3.f, kBias = 5.f;
 constexpr int kMaxSlots = 8;   // pages per tile (page_size 16)
+constexpr int kSetup = 1;      // tiles that a unit's queries and epilogue cost
 
 constexpr int pad16(int n) { return (n + 15) / 16 * 16; }
 constexpr int pow2_at_least(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
@@ -207,14 +208,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
-        const PagedRange r = paged_plan<RC>(a, gridDim.x, blockIdx.x);
+        const PagedRange r = paged_plan<RC, kSetup>(a, gridDim.x, blockIdx.x);
         if (lane == 0) ms.range = r;
     }
     __syncthreads();
-    const int64_t begin = ms.range.begin, end = ms.range.end;
-    int j0 = ms.range.j0;  // first tile of the segment in its unit
-    PagedWalk<RC> walk(a, ms.range);
-    if (begin >= end) walk.u.n = 0;
+    PagedWalk<RC, kSetup> walk(a, ms.range);
     const int G = (int)a.G.d;
     const int slots = kTile / a.page;
     if (blockIdx.x == 0 && warp == 4 && a.seqs.status)
@@ -231,9 +229,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int page_log = 31 - __clz(a.page);
         bool missing = false;
 #pragma unroll 1
-        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+        for (; walk.live(); walk.next()) {
             const PagedUnit u = walk.u;
-            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            const int j0 = walk.j0, j1 = walk.j1;
             const int32_t* row = a.seqs.table + walk.b * a.seqs.table_stride;
             // this lane's page of a tile, -1 where no row sees it
             auto fetch = [&](int j) -> int {
@@ -268,8 +266,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mbar_arrive_cp_async(full);
                 id = next;
             }
-            x += j1 - j0;
-            if (x < end) walk.next();
         }
         if (missing) paged_report(a.seqs, kBadPage);
 #pragma unroll 1
@@ -282,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             constexpr uint32_t id_o = mma_idesc(128, N2, true, true);    // V^T (channels) x weights
             uint32_t seg = 0;
 #pragma unroll 1
-            for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0, ++seg) {
-                const int cnt = end - x < walk.u.n - j0 ? (int)(end - x) : walk.u.n - j0;
+            for (; walk.live(); walk.next(), ++seg) {
+                const int cnt = walk.j1 - walk.j0;
                 wait(smem_u32(&ms.q_ready), seg & 1);
 #pragma unroll 1
                 for (int i = 0; i <= cnt; ++i) {
@@ -313,8 +309,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
                 it += cnt;
-                x += cnt;
-                if (x < end) walk.next();
             }
         }
         __syncwarp();
@@ -324,9 +318,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int page_log = 31 - __clz(a.page), slot = tid >> page_log;
         const uint32_t all_slots = (1u << slots) - 1u;
 #pragma unroll 1
-        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+        for (; walk.live(); walk.next()) {
             const PagedUnit u = walk.u;
-            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            const int j0 = walk.j0, j1 = walk.j1;
             const uint32_t real = u.rows >= 32 ? kFull : (1u << u.rows) - 1u;
             bar_tokens();  // the segment before is done with the row data
             write_queries<RC, QP, QT>(a, u, walk.h, sm + Sh::kQ, ms);
@@ -510,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             tc_fence_before();
-            const bool complete = j0 == 0 && j1 == u.n;
-            float* part = a.part + (int64_t)(2 * blockIdx.x + (x == begin ? 0 : 1)) * part_stride<RC>();
+            const bool complete = walk.complete();
+            float* part = a.part + (int64_t)(2 * blockIdx.x + (walk.first ? 0 : 1)) * part_stride<RC>();
 #pragma unroll
             for (int r = 0; r < RC; ++r) {
                 if (r >= u.rows) continue;
@@ -526,8 +520,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int rr = u.r0 + r, i = (int)fdiv((uint32_t)rr, a.G);
                 store_out(a, (int64_t)(u.row0 + i) * a.Hq + walk.h * G + rr - i * G, tid, sum == 0.f ? 0.f : v / sum);
             }
-            x += j1 - j0;
-            if (x < end) walk.next();
         }
     }
     if (!wait.good) paged_report(a.seqs, kTimeout);

@@ -3,9 +3,11 @@
 // the 128-token tiles that some row of it sees. The units' tiles, laid end to
 // end (sequence, kv-head, group), are cut into equal ranges, one per CTA: no
 // CTA waits for a longer one, whatever the lengths, and a long context is
-// split by itself. A unit inside one range is finished by its CTA; parts of
-// a unit that spans ranges go to the workspace and are joined by a second
-// kernel. Lengths are on the device, so a warp of each CTA derives its range.
+// split by itself. Each unit counts kSetup tiles more, in front of its own,
+// for what a CTA spends on a unit besides its tiles. A unit inside one range
+// is finished by its CTA; parts of a unit that spans ranges go to the
+// workspace and are joined by a second kernel. Lengths are on the device, so
+// a warp of each CTA derives its range.
 #pragma once
 
 #include "paged.cuh"
@@ -34,7 +36,7 @@ struct PagedUnit {
 // Where a CTA's range begins and ends, and the unit it begins in.
 struct PagedRange {
     int64_t begin, end;
-    int b, h, g, j0;  // j0: first tile of the range in its unit
+    int b, h, g, at;  // at: where in the unit the range begins, setup tiles counted
 };
 
 // A unit that crosses from CTA c - 1 into CTA c and began in c - 1 (kept by c):
@@ -71,22 +73,50 @@ __device__ __forceinline__ PagedUnit paged_unit(const PagedAttnArgs& a, const Pa
     return v;
 }
 
-// The units of a CTA's range, one after the other.
-template <int RC>
+// The segments of a CTA's range: tiles [j0, j1) of a unit, one after the other.
+//   for (PagedWalk<RC, kSetup> w(a, range); w.live(); w.next()) ...
+template <int RC, int kSetup>
 struct PagedWalk {
     const PagedAttnArgs& a;
     PagedSeq s;
     int b, h, g, groups;
+    int j0, j1;
+    bool first;      // the range began in this unit
+    int64_t left;    // of the range, this unit's share included
     PagedUnit u;
 
     __device__ __forceinline__ PagedWalk(const PagedAttnArgs& args, const PagedRange& r)
-        : a(args), b(r.b), h(r.h), g(r.g) {
+        : a(args), b(r.b), h(r.h), g(r.g), first(true), left(r.end - r.begin) {
+        if (left <= 0) return;
         s = paged_seq(a.seqs, b);
         groups = paged_groups<RC>(a, s);
         u = paged_unit<RC>(a, s, g);
+        share(r.at);
+        if (j0 >= j1) next();
+    }
+    __device__ __forceinline__ bool live() const { return left > 0; }
+    __device__ __forceinline__ bool complete() const { return j0 == 0 && j1 == u.n; }
+    __device__ __forceinline__ void next() {
+        do {
+            left -= taken;
+            first = false;
+            if (left <= 0) return;
+            next_unit();
+            if (u.n == 0) left = 0;  // the lengths changed under the call
+            share(0);
+        } while (left > 0 && j0 >= j1);
+    }
+
+private:
+    int taken;
+    __device__ __forceinline__ void share(int at) {
+        const int end = left < u.n + kSetup - at ? at + (int)left : u.n + kSetup;
+        taken = end - at;
+        j0 = at > kSetup ? at - kSetup : 0;
+        j1 = end > kSetup ? end - kSetup : 0;
     }
     // The next unit that has tiles; past the last one, u.n = 0.
-    __device__ __forceinline__ void next() {
+    __device__ __forceinline__ void next_unit() {
         do {
             if (++g >= groups) {
                 g = 0;
@@ -107,11 +137,14 @@ struct PagedWalk {
     }
 };
 
+template <int kSetup>
+__device__ __forceinline__ int paged_length(const PagedUnit& u) { return u.n ? u.n + kSetup : 0; }
+
 // The tiles of this lane's sequence of chunk b0 .. b0 + 31, for one kv-head.
 // Every lane of the warp calls it together. Sequences of a few groups are
 // summed by their lane, longer ones by the warp (a prompt has tens of groups
 // and may be the only sequence).
-template <int RC>
+template <int RC, int kSetup>
 __device__ __noinline__ int64_t paged_head_tiles(const PagedAttnArgs& a, int b0) {
     constexpr int kFew = 2;
     const int lane = lane_id();
@@ -123,7 +156,7 @@ __device__ __noinline__ int64_t paged_head_tiles(const PagedAttnArgs& a, int b0)
     }
     int64_t t = 0;
 #pragma unroll 1
-    for (int i = 0; i < n && n <= kFew; ++i) t += paged_unit<RC>(a, q, i).n;
+    for (int i = 0; i < n && n <= kFew; ++i) t += paged_length<kSetup>(paged_unit<RC>(a, q, i));
 #pragma unroll 1
     for (unsigned many = __ballot_sync(kFull, n > kFew); many; many &= many - 1) {
         const int src = __ffs(many) - 1;
@@ -133,7 +166,7 @@ __device__ __noinline__ int64_t paged_head_tiles(const PagedAttnArgs& a, int b0)
         const int m = __shfl_sync(kFull, n, src);
         int64_t part = 0;
 #pragma unroll 1
-        for (int i = lane; i < m; i += 32) part += paged_unit<RC>(a, o, i).n;
+        for (int i = lane; i < m; i += 32) part += paged_length<kSetup>(paged_unit<RC>(a, o, i));
 #pragma unroll
         for (int k = 16; k; k >>= 1) part += __shfl_xor_sync(kFull, part, k);
         if (lane == src) t = part;
@@ -154,14 +187,14 @@ __device__ __forceinline__ int64_t warp_prefix(int64_t v) {  // inclusive
 // The range of CTA c of `grid`, and the seam in front of it. With fewer tiles
 // than CTAs, the first `total` take one each. Every lane of one warp calls it
 // together; all get the result.
-template <int RC>
+template <int RC, int kSetup>
 __device__ __noinline__ PagedRange paged_plan(const PagedAttnArgs& a, int grid, int c) {
     const int lane = lane_id();
     PagedRange r{};
     int64_t total = 0, first_chunk = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < a.seqs.B; b0 += 32) {
-        const int64_t mine = paged_head_tiles<RC>(a, b0);
+        const int64_t mine = paged_head_tiles<RC, kSetup>(a, b0);
         if (b0 == 0) first_chunk = mine;
         total += mine;
     }
@@ -180,7 +213,7 @@ __device__ __noinline__ PagedRange paged_plan(const PagedAttnArgs& a, int grid, 
         int64_t x = r.begin, before = 0, per_head = 1;
 #pragma unroll 1
         for (int b0 = 0; b0 < a.seqs.B; b0 += 32) {
-            const int64_t mine = b0 ? paged_head_tiles<RC>(a, b0) : first_chunk;
+            const int64_t mine = b0 ? paged_head_tiles<RC, kSetup>(a, b0) : first_chunk;
             const int64_t incl = warp_prefix(mine * a.Hkv);
             const unsigned hit = __ballot_sync(kFull, x < before + incl);
             if (hit) {
@@ -198,7 +231,7 @@ __device__ __noinline__ PagedRange paged_plan(const PagedAttnArgs& a, int grid, 
         x -= r.h * per_head;
 #pragma unroll 1
         for (int g0 = 0; g0 < groups; g0 += 32) {
-            const int64_t mine = g0 + lane < groups ? paged_unit<RC>(a, s, g0 + lane).n : 0;
+            const int64_t mine = g0 + lane < groups ? paged_length<kSetup>(paged_unit<RC>(a, s, g0 + lane)) : 0;
             const int64_t incl = warp_prefix(mine);
             const unsigned hit = __ballot_sync(kFull, x < incl);
             if (hit) {
@@ -209,14 +242,15 @@ __device__ __noinline__ PagedRange paged_plan(const PagedAttnArgs& a, int grid, 
             }
             x -= __shfl_sync(kFull, incl, 31);
         }
-        r.j0 = (int)x;
+        r.at = (int)x;
         const PagedUnit u = paged_unit<RC>(a, s, r.g);
-        const int64_t u0 = r.begin - r.j0;
-        if (c > 0 && r.j0 > 0 && u0 >= prev) {
+        const int64_t u0 = r.begin - r.at;
+        // CTA c - 1 holds the unit's first tile, and this one a later one
+        if (c > 0 && r.at > kSetup && prev <= u0 + kSetup) {
             seam.live = 1;
-            seam.first = 2 * (c - 1) + (u0 > prev ? 1 : 0);
+            seam.first = 2 * (c - 1) + (prev >= u0 ? 0 : 1);
             // the CTA of the unit's last tile x: the last k with edge(k) <= x
-            seam.last = (int)(((u0 + u.n) * n - 1) / total);
+            seam.last = (int)(((u0 + u.n + kSetup) * n - 1) / total);
             seam.row0 = u.row0;
             seam.r0 = u.r0;
             seam.rows = u.rows;

@@ -28,16 +28,10 @@ namespace {
 
 constexpr int RC = 256;         // rows of a unit
 constexpr int kThreads = 512;   // warps 0-3, 4-7: rows; 8-11: V to fp16; 12: TMA; 13: MMA issue
-// Registers a thread of each warpgroup: together the 512 x 128 of the launch.
-constexpr int kRowRegs = 184, kValueRegs = 80, kIssueRegs = 64;
-static_assert(2 * kRowRegs + kValueRegs + kIssueRegs == 4 * 128, "register split");
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr float kLag = 8.f, kBias = 6.f;
 constexpr int kKStages = 3, kRing = 8;
 constexpr int kMaxSlots = 8;
+constexpr int kSetup = 3;       // tiles that a unit's queries and epilogue cost
 
 // shared memory, from a 1024-aligned base
 constexpr uint32_t kQ = 0;                        // [half][piece][128 rows][128 B]
@@ -62,52 +56,67 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
     return r;
 }
 
-// One row's query as two e4m3 pieces; returns its scale.
-__device__ __forceinline__ float write_row(const PagedAttnArgs& a, const __nv_bfloat16* q, bool real, uint8_t* hi,
-                                           int row) {
-    uint8_t* lo = hi + 16384;
-    float top = 0.f;
-    bool bad = false;
-    if (real) {
-#pragma unroll 4
-        for (int i = 0; i < kD / 4; ++i) {
-            float x[4];
-            load4(q + 4 * i, x);
+// Queries of the warp's 32 rows (from unit row `first` on) as two e4m3 pieces,
+// eight lanes to a row, 16 channels each; returns the scale of this lane's row.
+__device__ __forceinline__ float write_rows(const PagedAttnArgs& a, const PagedUnit& u, int h, int first, uint8_t* hi,
+                                            int lrow0) {
+    const int lane = lane_id(), c = lane & 7, G = (int)a.G.d;
+    float mine = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+        const int r = first + 4 * i + (lane >> 3);
+        float x[16];
+        float top = 0.f;
+        bool bad = false;
+        if (r < u.rows) {
+            const int rr = u.r0 + r, qi = (int)fdiv((uint32_t)rr, a.G);
+            const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                            (int64_t)(u.row0 + qi) * a.q_st +
+                                                            (int64_t)(h * G + rr - qi * G) * a.q_sh + 16 * c);
+            const uint4 w0 = q[0], w1 = q[1];
+            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                top = fmaxf(top, fabsf(x[k]));
-                bad |= !isfinite(x[k]);
+            for (int k = 0; k < 8; ++k) {
+                x[2 * k] = __uint_as_float(w[k] << 16);
+                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
             }
-        }
-    }
-    // the least e >= -126 with top <= 448 * 2^e
-    const uint32_t bits = __float_as_uint(top);
-    int e = (int)(bits >> 23) - 127 - ((bits & 0x7fffffu) > 0x600000u ? 7 : 8);
-    e = bad ? 0 : (e < -126 ? -126 : e);
-    float up = __uint_as_float((uint32_t)(127 - e) << 23);
-    if (a.scale_log2 < 0.f) up = -up;
-#pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-        uint32_t h[4] = {0, 0, 0, 0}, l[4] = {0, 0, 0, 0};
-        if (real) {
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float x[4];
-                load4(q + 16 * c + 4 * i, x);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] *= up;
-                const uint32_t c0 = e4m3x2(x[0], x[1]), c1 = e4m3x2(x[2], x[3]);
-                const uint32_t h0 = e4m3x2_to_f16x2(c0), h1 = e4m3x2_to_f16x2(c1);
-                h[i] = bad ? 0x7f7f7f7fu : (c0 | (c1 << 16));
-                l[i] = bad ? 0u : (e4m3x2(x[0] - f16_lo(h0), x[1] - f16_hi(h0)) |
-                                   (e4m3x2(x[2] - f16_lo(h1), x[3] - f16_hi(h1)) << 16));
-            }
+            for (int k = 0; k < 16; ++k) x[k] = 0.f;
         }
-        const int at = row * 128 + ((c ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            top = fmaxf(top, fabsf(x[k]));
+            bad |= !isfinite(x[k]);
+        }
+#pragma unroll
+        for (int m = 4; m; m >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, m));
+        bad = ((__ballot_sync(kFull, bad) >> (lane & 24)) & 0xffu) != 0;
+        // the least e >= -126 with top <= 448 * 2^e
+        const uint32_t bits = __float_as_uint(top);
+        int e = (int)(bits >> 23) - 127 - ((bits & 0x7fffffu) > 0x600000u ? 7 : 8);
+        e = bad ? 0 : (e < -126 ? -126 : e);
+        const float scale = __shfl_sync(kFull, __uint_as_float((uint32_t)(127 + e) << 23), (lane & 3) << 3);
+        if ((lane >> 2) == i) mine = scale;
+        float up = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (a.scale_log2 < 0.f) up = -up;
+        uint32_t p[4], l[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float y[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) y[m] = x[4 * k + m] * up;
+            const uint32_t c0 = e4m3x2(y[0], y[1]), c1 = e4m3x2(y[2], y[3]);
+            const uint32_t h0 = e4m3x2_to_f16x2(c0), h1 = e4m3x2_to_f16x2(c1);
+            p[k] = bad ? 0x7f7f7f7fu : (c0 | (c1 << 16));
+            l[k] = bad ? 0u : (e4m3x2(y[0] - f16_lo(h0), y[1] - f16_hi(h0)) |
+                               (e4m3x2(y[2] - f16_lo(h1), y[3] - f16_hi(h1)) << 16));
+        }
+        const int lrow = lrow0 + 4 * i + (lane >> 3), at = lrow * 128 + ((c ^ (lrow & 7)) << 4);
+        *reinterpret_cast<uint4*>(hi + at) = make_uint4(p[0], p[1], p[2], p[3]);
+        *reinterpret_cast<uint4*>(hi + 16384 + at) = make_uint4(l[0], l[1], l[2], l[3]);
     }
-    return fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23);
+    return mine * fabsf(a.scale_log2);
 }
 
 // A row's view of a tile: columns up to hi and above lo, or below sink, on
@@ -280,14 +289,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
-        const PagedRange r = paged_plan<RC>(a, gridDim.x, blockIdx.x);
+        const PagedRange r = paged_plan<RC, kSetup>(a, gridDim.x, blockIdx.x);
         if (lane == 0) ms.range = r;
     }
     __syncthreads();
-    const int64_t begin = ms.range.begin, end = ms.range.end;
-    int j0 = ms.range.j0;  // first tile of the segment in its unit
-    PagedWalk<RC> walk(a, ms.range);
-    if (begin >= end) walk.u.n = 0;
+    PagedWalk<RC, kSetup> walk(a, ms.range);
     const int G = (int)a.G.d, slots = kTile / a.page, page_log = 31 - __clz(a.page);
     if (blockIdx.x == 0 && warp == 12 && a.seqs.status)
 #pragma unroll 1
@@ -299,14 +305,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;  // tiles of this CTA so far
 
     if (warp >= 12) {
-        regs_dec<kIssueRegs>();
         if (warp == 12) {
         // ------------------------------------------------------------ TMA --
         bool missing = false;
 #pragma unroll 1
-        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+        for (; walk.live(); walk.next()) {
             const PagedUnit u = walk.u;
-            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            const int j0 = walk.j0, j1 = walk.j1;
             const int32_t* row = a.seqs.table + walk.b * a.seqs.table_stride;
             auto fetch = [&](int j) -> int {  // this lane's page of a tile, -1 where no row sees it
                 if (lane >= slots || j >= j1) return -1;
@@ -346,8 +351,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (id >= 0) tma_tile(sb + kV + vs * 16384u + off, &maps.v, tile, v_full);
                 id = next;
             }
-            x += j1 - j0;
-            if (x < end) walk.next();
         }
         if (missing) paged_report(a.seqs, kBadPage);
 #pragma unroll 1
@@ -361,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_s = mma_idesc(128, 128, false, false), id_o = mma_idesc(128, 128, false, true);
             uint32_t seg[2] = {0, 0}, np[2] = {0, 0};  // segments and weight tiles of each half
 #pragma unroll 1
-            for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
-                const int cnt = end - x < walk.u.n - j0 ? (int)(end - x) : walk.u.n - j0;
+            for (; walk.live(); walk.next()) {
+                const int cnt = walk.j1 - walk.j0;
                 const int halves = walk.u.rows > 128 ? 2 : 1;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)
@@ -401,21 +404,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (i < cnt) mma_commit(smem_u32(&ms.k_empty[t % kKStages]));
                 }
                 it += cnt;
-                x += cnt;
-                if (x < end) walk.next();
             }
         }
         __syncwarp();
         }
     } else if (warp >= 8) {
         // -------------------------------------------------- V to fp16 tiles --
-        regs_dec<kValueRegs>();
         const int tok = tid - 256;  // token of the tile
         uint32_t seg[2] = {0, 0};
 #pragma unroll 1
-        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+        for (; walk.live(); walk.next()) {
             const PagedUnit u = walk.u;
-            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            const int j0 = walk.j0, j1 = walk.j1;
             wait(smem_u32(&ms.q_ready[0]), seg[0]++ & 1);  // the rows' NaN marks are clear
             if (u.rows > 128) wait(smem_u32(&ms.q_ready[1]), seg[1]++ & 1);
 #pragma unroll 1
@@ -467,21 +467,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(smem_u32(&ms.v_empty[buf]));
                 }
             }
-            x += j1 - j0;
-            if (x < end) walk.next();
         }
     } else {
         // ------------------------------------------------------------ rows --
-        regs_inc<kRowRegs>();
-        const int hf = warp >> 2, lrow = tid & 127, r = tid;  // r: row of the unit
+        const int hf = warp >> 2, r = tid;  // r: row of the unit
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + hf * 128, o_at = tmem + lanes + 256 + hf * 128;
         const uint32_t all_slots = (1u << slots) - 1u;
         uint32_t n = 0, seg = 0;  // weight tiles and segments of this half
 #pragma unroll 1
-        for (int64_t x = begin; x < end && walk.u.n > 0; j0 = 0) {
+        for (; walk.live(); walk.next()) {
             const PagedUnit u = walk.u;
-            const int j1 = end - x < u.n - j0 ? j0 + (int)(end - x) : u.n;
+            const int j0 = walk.j0, j1 = walk.j1;
             if (hf * 128 < u.rows) {
                 const bool real = r < u.rows;
                 const int rr = u.r0 + (real ? r : 0), qi = (int)fdiv((uint32_t)rr, a.G);
@@ -492,9 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int wn = u.rows - 32 * warp < 32 ? u.rows - 32 * warp : 32;
                 const int wp0 = u.first_pos + (int)fdiv((uint32_t)w0, a.G);
                 const int wp1 = u.first_pos + (int)fdiv((uint32_t)(w0 + (wn > 0 ? wn : 1) - 1), a.G);
-                const float c = write_row(a, reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                 (int64_t)(u.row0 + qi) * a.q_st + (int64_t)(walk.h * G + rr - qi * G) * a.q_sh,
-                                          real, sm + kQ + hf * 32768, lrow);
+                const float c = write_rows(a, u, walk.h, 32 * warp, sm + kQ + hf * 32768, 32 * (warp & 3));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) ms.nan[r][k] = 0u;
                 proxy_fence();
@@ -531,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 wait(smem_u32(&ms.o_full[hf]), seg++ & 1);
                 tc_fence_after();
-                const bool complete = j0 == 0 && j1 == u.n;
-                float* part = a.part + (2 * blockIdx.x + (x == begin ? 0 : 1)) * part_stride<RC>();
+                const bool complete = walk.complete();
+                float* part = a.part + (2 * blockIdx.x + (walk.first ? 0 : 1)) * part_stride<RC>();
                 const float inv = complete ? (st.l == 0.f ? 0.f : st.vref / st.l) : st.vref;
                 __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + out_row * kD;
 #pragma unroll 1
@@ -563,8 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 it += j1 - j0;
             }
-            x += j1 - j0;
-            if (x < end) walk.next();
         }
     }
     if (!wait.good) paged_report(a.seqs, kTimeout);
