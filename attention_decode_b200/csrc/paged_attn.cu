@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(sm);
     Misc& ms = *reinterpret_cast<Misc*>(sm + Sh::kMisc);
-    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
+    const int tid = threadIdx.x, lane = lane_id(), warp = __shfl_sync(kFull, tid >> 5, 0);
 
     if (tid == 0) {
 #pragma unroll 1
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             wait(smem_u32(&ms.full[i % ST]), (i / ST) & 1);
     } else if (warp == 5) {
         // ------------------------------------------------------------ MMA --
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id_s = mma_idesc(128, N1, false, false);  // K rows x query columns
             constexpr uint32_t id_o = mma_idesc(128, N2, true, true);    // V^T (channels) x weights
             uint32_t seg = 0;

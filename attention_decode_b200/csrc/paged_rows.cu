@@ -11,7 +11,7 @@
 //   O += P V       kind::f16, P from TMEM (over S), V widened to fp16 (exact)
 //                  in shared memory by a warpgroup of its own.
 // fp16 weights keep 11 bits; the running maximum may lag by 2^kLag and the
-// bias 2^kBias keeps the largest below 2^14 and the smallest at 2^-30.
+// bias 2^kBias keeps the largest below 2^15 and the smallest at 2^-27.
 //
 // What bounds it: the tensor cores (2 x 512 clocks per half and tile) and the
 // exponentials (16384 per half and tile, 16 a clock: 1024 clocks). The halves
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int RC = 256;         // rows of a unit
 constexpr int kThreads = 512;   // warps 0-3, 4-7: rows; 8-11: V to fp16; 12: TMA; 13: MMA issue
-constexpr float kLag = 8.f, kBias = 6.f;
+constexpr float kLag = 12.f, kBias = 3.f;
 constexpr int kKStages = 3, kRing = 8;
 constexpr int kMaxSlots = 8;
 constexpr int kSetup = 3;       // tiles that a unit's queries and epilogue cost
@@ -42,7 +42,7 @@ constexpr uint32_t kMisc = kV16 + 4 * 16384;
 
 struct Misc {
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2], w_full[2], w_free[2], sc_full[kRing];
-    uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_ready[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2];
     uint32_t tmem;
     PagedRange range;
     uint32_t ok[kRing];                // pages of the tile that were loaded
@@ -62,27 +62,31 @@ __device__ __forceinline__ float write_rows(const PagedAttnArgs& a, const PagedU
                                             int lrow0) {
     const int lane = lane_id(), c = lane & 7, G = (int)a.G.d;
     float mine = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
+    uint4 raw[8][2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // every load first: their latencies overlap
         const int r = first + 4 * i + (lane >> 3);
-        float x[16];
-        float top = 0.f;
-        bool bad = false;
+        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
         if (r < u.rows) {
             const int rr = u.r0 + r, qi = (int)fdiv((uint32_t)rr, a.G);
             const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
                                                             (int64_t)(u.row0 + qi) * a.q_st +
                                                             (int64_t)(h * G + rr - qi * G) * a.q_sh + 16 * c);
-            const uint4 w0 = q[0], w1 = q[1];
-            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            raw[i][0] = q[0];
+            raw[i][1] = q[1];
+        }
+    }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                x[2 * k] = __uint_as_float(w[k] << 16);
-                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-            }
-        } else {
+    for (int i = 0; i < 8; ++i) {
+        const uint4 w0 = raw[i][0], w1 = raw[i][1];
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        float x[16];
+        float top = 0.f;
+        bool bad = false;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = 0.f;
+        for (int k = 0; k < 8; ++k) {
+            x[2 * k] = __uint_as_float(w[k] << 16);
+            x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -141,114 +145,125 @@ struct RowState {
     float vref, rv;    // largest v scale so far and its reciprocal
 };
 
-// Multiplies a row's weights of the tile so far (`done` columns of fp16 pairs)
-// and, behind the first tile, its output by a factor.
-__device__ __noinline__ void rescale_row(uint32_t s, int done, uint32_t o, bool have_o, float fp, float fo) {
-    const uint32_t f2 = f16x2(fp, fp);
-#pragma unroll 1
-    for (int i = 0; i < done; i += 8) {
-        float v[8];
-        tmem_ld<8>(s + i, v);
+// Multiplies a row's weights of the step so far (`done` columns of fp16 pairs,
+// 0 or 16) and, if there is one, its output by a factor.
+__device__ __noinline__ void rescale_row(uint32_t s, int done, uint32_t o, bool have_o, float f) {
+    if (done) {
+        const uint32_t f2 = f16x2(f, f);
+        uint32_t u[16];
+        TmemLoad<16>::run(s, u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            uint32_t h = __float_as_uint(v[k]);
-            asm("mul.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(f2));
-            v[k] = __uint_as_float(h);
-        }
-        tmem_st8(s + i, v);
+        for (int k = 0; k < 16; ++k) asm("mul.f16x2 %0, %1, %2;" : "=r"(u[k]) : "r"(u[k]), "r"(f2));
+        tmem_st16(s, u);
     }
 #pragma unroll 1
-    for (int i = 0; have_o && i < kD; i += 8) {
-        float v[8];
-        tmem_ld<8>(o + i, v);
+    for (int i = 0; have_o && i < kD; i += 16) {
+        uint32_t u[16];
+        TmemLoad<16>::run(o + i, u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= fo;
-        tmem_st8(o + i, v);
+        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f);
+        tmem_st16(o + i, u);
     }
     tmem_wait_st();
 }
 
-// The weights of a row over a tile, 32 columns at a time, in fp16 pairs over
-// the front of its scores: column pair i of P takes the place of score i,
-// which has been read by then. Where a chunk's largest exponent passes the
-// lag, the warp raises its rows' maxima to that chunk's.
+// Weights of 32 columns of a row from their scores u: exponents, the largest
+// of them, 2^x, their sum; packed in fp16 pairs.
 template <bool MASKED>
-__device__ __forceinline__ void row_tile(uint32_t s, uint32_t o, bool have_o, const float2* scale, int page_log,
-                                         bool real, const View& view, RowState& st) {
+__device__ __forceinline__ void row_weights(const uint32_t (&u)[32], uint32_t seen, const float2 (&kv)[2],
+                                            const RowState& st, float& most, float& sum, uint32_t (&p)[16]) {
+    const uint64_t nm = pk2(kBias - st.m, kBias - st.m);
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const float f = kv[g].x * st.c, w = kv[g].y * st.rv;
+        const uint64_t f2 = pk2(f, f), w2 = pk2(w, w);
+        const bool weigh = w != 1.f;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const int at = 16 * g + i;
+            float2 x = upk2(fma2(pk2(__uint_as_float(u[at]), __uint_as_float(u[at + 1])), f2, nm));
+            if (MASKED) {
+                x.x = (seen >> at) & 1u ? x.x : -INFINITY;
+                x.y = (seen >> at) & 2u ? x.y : -INFINITY;
+            }
+            top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(x.x, x.y));
+            v[i] = exp2_approx(x.x);
+            v[i + 1] = exp2_approx(x.y);
+            acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pk2(v[i], v[i + 1]));
+        }
+        if (weigh) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                float2 y = upk2(mul2(pk2(v[i], v[i + 1]), w2));
+                if (MASKED) {  // the scale of a page that was not loaded is void
+                    y.x = (seen >> (16 * g + i)) & 1u ? y.x : 0.f;
+                    y.y = (seen >> (16 * g + i)) & 2u ? y.y : 0.f;
+                }
+                v[i] = y.x;
+                v[i + 1] = y.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) p[8 * g + i / 2] = f16x2(v[i], v[i + 1]);
+    }
+    most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    const float2 t = upk2(add2(acc[0], acc[1]));
+    sum = t.x + t.y;
+}
+
+// Raises a row's maximum to that of columns 32 q .. 32 q + 31 (their scores are
+// still in TMEM) and scales the weights and outputs so far; returns the new
+// maximum and the factor.
+__device__ __noinline__ float2 raise_row(uint32_t s, uint32_t o, bool have_o, int q, uint32_t seen, float f0, float f1,
+                                         bool real, float m) {
+    float top = -INFINITY;
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-        const uint32_t seen = MASKED ? view.bits(32 * q) : kFull;
-        float v[32], most;
-        float2 kv[2];
+    for (int i = 0; i < 32; i += 8) {
+        float v[8];
+        tmem_ld<8>(s + 32 * q + i, v);
+        const float f = i < 16 ? f0 : f1;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) kv[g] = scale[(32 * q + 16 * g) >> page_log];
-        auto exponents = [&]() {
-            tmem_ld<32>(s + 32 * q, v);
-            const uint64_t nm = pk2(kBias - st.m, kBias - st.m);
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const float f = kv[g].x * st.c;
-                const uint64_t f2 = pk2(f, f);
-#pragma unroll
-                for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                    float2 x = upk2(fma2(pk2(v[i], v[i + 1]), f2, nm));
-                    if (MASKED) {
-                        x.x = (seen >> i) & 1u ? x.x : -INFINITY;
-                        x.y = (seen >> i) & 2u ? x.y : -INFINITY;
-                    }
-                    v[i] = x.x;
-                    v[i + 1] = x.y;
-                    top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(x.x, x.y));
-                }
-            }
-            most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        };
-        exponents();
-        if (__any_sync(kFull, real && most > kBias + kLag)) {
-            // scores again, without the maximum (it may be -inf still)
-            const float m = st.m;
-            st.m = 0.f;
-            exponents();
-            most -= kBias;
-            const float mn = real ? fmaxf(m, most) : 0.f;
-            const float f = m == mn ? 1.f : exp2_approx(m - mn);
-            st.m = mn;
-            st.l *= f;
-            rescale_row(s, 16 * q, o, have_o, f, f);
-            exponents();
-        }
-        uint64_t acc0 = pk2(0.f, 0.f), acc1 = acc0;
+        for (int k = 0; k < 8; ++k)
+            if ((seen >> (i + k)) & 1u) top = fmaxf(top, v[k] * f);
+    }
+    const float mn = real ? fmaxf(m, top) : 0.f;
+    const float f = m == mn ? 1.f : exp2_approx(m - mn);
+    rescale_row(s, 16 * q, o, have_o, f);
+    return make_float2(mn, f);
+}
+
+// The weights of a row over step b of a tile (64 tokens), 32 columns at a time,
+// over the front of its scores: column pair i of P takes the place of score
+// i, which has been read by then. Where a chunk's largest exponent passes the
+// lag, the warp raises its rows' maxima first.
+template <bool MASKED>
+__device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, int b, const float2* scale, int page_log,
+                                         bool real, const View& view, RowState& st, Waiter& wait, uint32_t pv_done) {
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q) {
+        const int col = 64 * b + 32 * q;
+        const uint32_t seen = MASKED ? view.bits(col) : kFull;
+        const float2 kv[2] = {scale[col >> page_log], scale[(col + 16) >> page_log]};
+        uint32_t u[32];
+        TmemLoad<32>::run(s + 32 * q, u);
+        float most, sum;
         uint32_t p[16];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const float w = kv[g].y * st.rv;
-            const bool weigh = w != 1.f;
-#pragma unroll
-            for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                v[i] = exp2_approx(v[i]);
-                v[i + 1] = exp2_approx(v[i + 1]);
-                if (i & 2) acc1 = add2(acc1, pk2(v[i], v[i + 1]));
-                else acc0 = add2(acc0, pk2(v[i], v[i + 1]));
+        row_weights<MASKED>(u, seen, kv, st, most, sum, p);
+        if (__any_sync(kFull, real && most > kBias + kLag)) {
+            if (have_o) {  // O is quiet once the step before is done
+                wait(pv_done, b ^ 1);
+                tc_fence_after();
             }
-            if (weigh) {
-                const uint64_t w2 = pk2(w, w);
-#pragma unroll
-                for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                    float2 y = upk2(mul2(pk2(v[i], v[i + 1]), w2));
-                    if (MASKED) {  // the scale of a page that was not loaded is void
-                        y.x = (seen >> i) & 1u ? y.x : 0.f;
-                        y.y = (seen >> i) & 2u ? y.y : 0.f;
-                    }
-                    v[i] = y.x;
-                    v[i + 1] = y.y;
-                }
-            }
-#pragma unroll
-            for (int i = 16 * g; i < 16 * g + 16; i += 2) p[i / 2] = f16x2(v[i], v[i + 1]);
+            const float2 r = raise_row(s, o, have_o, q, seen, kv[0].x * st.c, kv[1].x * st.c, real, st.m);
+            st.m = r.x;
+            st.l *= r.y;
+            TmemLoad<32>::run(s + 32 * q, u);
+            row_weights<MASKED>(u, seen, kv, st, most, sum, p);
         }
-        const float2 t = upk2(add2(acc0, acc1));
-        st.l += t.x + t.y;
+        st.l += sum;
         tmem_st16(s + 16 * q, p);
     }
     tmem_wait_st();
@@ -260,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(sm);
     Misc& ms = *reinterpret_cast<Misc*>(sm + kMisc);
-    const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
+    const int tid = threadIdx.x, lane = lane_id(), warp = __shfl_sync(kFull, tid >> 5, 0);
 
     if (tid == 0) {
         for (int i = 0; i < kKStages; ++i) {
@@ -273,8 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ms.w_full[i]), 4);
             mbar_init(smem_u32(&ms.w_free[i]), 1);
             mbar_init(smem_u32(&ms.q_ready[i]), 4);
-            mbar_init(smem_u32(&ms.s_full[i]), 1);
-            mbar_init(smem_u32(&ms.p_full[i]), 4);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&ms.s_full[i][b]), 1);
+                mbar_init(smem_u32(&ms.p_full[i][b]), 4);
+            }
+            mbar_init(smem_u32(&ms.pv_done[i]), 1);
             mbar_init(smem_u32(&ms.o_full[i]), 1);
         }
         for (int i = 0; i < kRing; ++i) mbar_init(smem_u32(&ms.sc_full[i]), 33);
@@ -360,50 +378,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = it < 2 ? 0 : it - 2; i < it; ++i) wait(smem_u32(&ms.v_full[i & 1]), (i >> 1) & 1);
         } else if (warp == 13) {
         // ------------------------------------------------------------ MMA --
-        if (lane == 0) {
-            constexpr uint32_t id_s = mma_idesc(128, 128, false, false), id_o = mma_idesc(128, 128, false, true);
-            uint32_t seg[2] = {0, 0}, np[2] = {0, 0};  // segments and weight tiles of each half
+        if (elect_one()) {
+            // A step is 64 tokens: half of a tile. The scores of step i + 2 take the
+            // place of the weights of step i, behind their P V (MMAs of a CTA run in
+            // the order of issue), so that a half always has its next scores ready.
+            constexpr uint32_t id_s = mma_idesc(128, 64, false, false), id_o = mma_idesc(128, 128, false, true);
+            uint32_t seg[2] = {0, 0}, np[2] = {0, 0};  // segments and weight steps of each half
 #pragma unroll 1
             for (; walk.live(); walk.next()) {
-                const int cnt = walk.j1 - walk.j0;
+                const int cnt = 2 * (walk.j1 - walk.j0);
                 const int halves = walk.u.rows > 128 ? 2 : 1;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)
                     if (hf < halves) wait(smem_u32(&ms.q_ready[hf]), seg[hf]++ & 1);
 #pragma unroll 1
-                for (int i = 0; i <= cnt; ++i) {
-                    const uint32_t t = it + i, tp = t - 1;
+                for (int i = 0; i < cnt + 2; ++i) {
+                    const uint32_t t = it + (i >> 1), tp = t - 1, b = i & 1;
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         if (hf >= halves) continue;
-                        if (i > 0) {
-                            if (hf == 0) wait(smem_u32(&ms.w_full[tp & 1]), (tp >> 1) & 1);
-                            wait(smem_u32(&ms.p_full[hf]), np[hf]++ & 1);
+                        if (i > 1) {
+                            if (hf == 0 && b == 0) wait(smem_u32(&ms.w_full[tp & 1]), (tp >> 1) & 1);
+                            wait(smem_u32(&ms.p_full[hf][b]), (np[hf] >> 1) & 1);
+                            ++np[hf];
                             tc_fence_after();
-                            const uint64_t vb = desc_sw128(sb + kV16 + (tp & 1) * 32768u, 16384, 1024);
+                            const uint64_t vb = desc_sw128(sb + kV16 + (tp & 1) * 32768u + b * 8192u, 16384, 1024);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)  // 16 tokens each
-                                mma_f16_ts(tmem + 256 + hf * 128, tmem + hf * 128 + 8 * k, vb + 128 * k, id_o,
-                                           i > 1 || k > 0);
-                            if (i == cnt) mma_commit(smem_u32(&ms.o_full[hf]));
+                            for (int k = 0; k < 4; ++k)  // 16 tokens each
+                                mma_f16_ts(tmem + 256 + hf * 128, tmem + hf * 128 + b * 64 + 8 * k, vb + 128 * k, id_o,
+                                           i > 2 || k > 0);
+                            mma_commit(smem_u32(&ms.pv_done[hf]));
+                            if (i == cnt + 1) mma_commit(smem_u32(&ms.o_full[hf]));
                         }
                         if (i < cnt) {
-                            if (hf == 0) {
+                            if (hf == 0 && b == 0) {
                                 wait(smem_u32(&ms.k_full[t % kKStages]), (t / kKStages) & 1);
                                 tc_fence_after();
                             }
-                            const uint64_t kb = desc_sw128(sb + kK + (t % kKStages) * 16384u, 16, 1024);
+                            const uint64_t kb = desc_sw128(sb + kK + (t % kKStages) * 16384u + b * 8192u, 16, 1024);
                             const uint64_t qa = desc_sw128(sb + kQ + hf * 32768u, 16, 1024);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)  // 32 channels each; the pieces one after the other
-                                mma_f8(tmem + hf * 128, qa + (k >> 2) * 1024 + 2 * (k & 3), kb + 2 * (k & 3), id_s, k > 0);
-                            mma_commit(smem_u32(&ms.s_full[hf]));
+                                mma_f8(tmem + hf * 128 + b * 64, qa + (k >> 2) * 1024 + 2 * (k & 3), kb + 2 * (k & 3), id_s,
+                                       k > 0);
+                            mma_commit(smem_u32(&ms.s_full[hf][b]));
                         }
                     }
-                    if (i > 0) mma_commit(smem_u32(&ms.w_free[tp & 1]));
-                    if (i < cnt) mma_commit(smem_u32(&ms.k_empty[t % kKStages]));
+                    if (i > 1 && b == 1) mma_commit(smem_u32(&ms.w_free[tp & 1]));
+                    if (i < cnt && b == 1) mma_commit(smem_u32(&ms.k_empty[t % kKStages]));
                 }
-                it += cnt;
+                it += cnt >> 1;
             }
         }
         __syncwarp();
@@ -474,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + hf * 128, o_at = tmem + lanes + 256 + hf * 128;
         const uint32_t all_slots = (1u << slots) - 1u;
+        const uint32_t pv_done = smem_u32(&ms.pv_done[hf]);
         uint32_t n = 0, seg = 0;  // weight tiles and segments of this half
 #pragma unroll 1
         for (; walk.live(); walk.next()) {
@@ -499,30 +524,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int j = j0; j < j1; ++j, ++it, ++n) {
                     const uint32_t ring = it % kRing;
-                    wait(smem_u32(&ms.s_full[hf]), n & 1);
                     wait(smem_u32(&ms.sc_full[ring]), (it / kRing) & 1);
-                    tc_fence_after();
                     const int t0 = u.tile(j) * kTile;
                     const uint32_t ok = ms.ok[ring];
                     const float2* scale = ms.scale[ring];
                     const bool whole = ok == all_slots && t0 + kTile - 1 <= wp0 &&
                                        (!a.window || t0 > wp1 - a.window || t0 + kTile <= a.sinks);
                     const View view{pos - t0, a.window ? pos - t0 - a.window : -1, a.sinks - t0, ok, page_log};
-                    float vmax = 0.f;
+                    // (scales are positive: their bits order like them)
+                    const float vmax = __uint_as_float(__reduce_max_sync(
+                        kFull, lane < slots && ((ok >> lane) & 1u) ? __float_as_uint(scale[lane].y) : 0u));
 #pragma unroll 1
-                    for (int i = 0; i < slots; ++i)
-                        if ((ok >> i) & 1u) vmax = fmaxf(vmax, scale[i].y);
-                    // O is quiet: P V of the tile before came in front of this S
-                    if (vmax > st.vref) {
-                        rescale_row(s_at, 0, o_at, j > j0, 1.f, st.vref / vmax);
-                        st.vref = vmax;
-                        st.rv = 1.f / vmax;
+                    for (int b = 0; b < 2; ++b) {
+                        wait(smem_u32(&ms.s_full[hf][b]), n & 1);
+                        tc_fence_after();
+                        const bool have_o = j > j0 || b > 0;
+                        if (vmax > st.vref) {
+                            if (have_o) {  // O is quiet once the step before is done; the one in
+                                           // front of that is, it came before these scores
+                                wait(pv_done, b ^ 1);
+                                tc_fence_after();
+                                rescale_row(s_at, 0, o_at, true, st.vref / vmax);
+                            }
+                            st.vref = vmax;
+                            st.rv = 1.f / vmax;
+                        }
+                        if (whole) row_step<false>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
+                        else row_step<true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&ms.p_full[hf][b]));
                     }
-                    if (whole) row_tile<false>(s_at, o_at, j > j0, scale, page_log, real, view, st);
-                    else row_tile<true>(s_at, o_at, j > j0, scale, page_log, real, view, st);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&ms.p_full[hf]));
                 }
                 wait(smem_u32(&ms.o_full[hf]), seg++ & 1);
                 tc_fence_after();
