@@ -115,7 +115,10 @@ nsnq_status nsnq_paged_append(const void* k, const void* v, const void* q, void*
     // a sequence of n rows touches at most n / page + 2 pages, and at most n
     const int64_t most = n_rows / a.page + 2 * (int64_t)B;
     a.items = n_rows < most ? n_rows : most;
-    for (int i = 0; i < D / 2 && a.rope; ++i) a.freq[i] = pow(rope_base, -2.0 * i / D);
+    for (int i = 0; i < D / 2 && a.rope; ++i) {
+        a.freq[i] = pow(rope_base, -2.0 * i / D);
+        a.turns[i] = a.freq[i] / 6.283185307179586476925;
+    }
     const cudaError_t e = nsnq::launch_paged_append(a, dtype == NSNQ_BF16, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return set_error(NSNQ_ERR_CUDA, "paged append launch: %s", cudaGetErrorString(e));
     return ok();

@@ -37,9 +37,11 @@ struct PagedAppendArgs {
     int64_t num_pages;
     int page;
     int64_t items;       // page slots the grid covers (an upper bound of those written)
-    double freq[kD / 2];  // rope_base^(-2i/D)
+    int heads;            // heads a block takes (set by the launcher)
+    double freq[kD / 2];  // rope_base^(-2i/D): radians a token
+    double turns[kD / 2];  // the same in turns
 };
-cudaError_t launch_paged_append(const PagedAppendArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_paged_append(PagedAppendArgs a, bool bf16, cudaStream_t s);
 
 struct PagedAttnArgs {
     PagedSeqs seqs;

@@ -3,9 +3,17 @@
 // scale per (page, head).
 //
 // x -> code = e4m3(x / 2^e), e the least exponent with every |x| of the
-// (page, head) <= 448 * 2^e. One block owns one (page, head) of K or V, so
+// (page, head) <= 448 * 2^e. One block owns a page for its heads of K or V, so
 // the page's scale, the codes of its new tokens and, where the scale grows,
 // the renewed codes of its older tokens have a single writer and no atomics.
+//
+// Codes and scales are those of the fp64 rotation, decided in fp32: angles are
+// reduced in fp64, cos and sin rounded to fp32, and a rotated value is then
+// off by at most 2^-22 (|x| + |y|) of its pair (x, y). Where a code or scale
+// would change within twice that, it is decided again from an fp64 rotation
+// (about one code in 10^5). The cos and sin of a page's rows are computed once
+// per block, in shared memory, and serve all its heads.
+//
 #include <math.h>
 
 #include "paged.cuh"
@@ -14,7 +22,14 @@ namespace nsnq {
 
 namespace {
 
-constexpr int kAppThreads = 128;  // 16 rows of 8 lanes; a lane holds channels [8l, 8l+8) of both halves
+// A row is 8 lanes, lane l holding channels [8l, 8l + 8) of both halves (the
+// rotation's pairs). A thread takes kPasses rows of a page.
+template <int PAGE>
+struct AppShape {
+    static constexpr int kThreads = PAGE == 128 ? 256 : 128;
+    static constexpr int kPasses = PAGE * 8 / kThreads;
+};
+constexpr float kErr = 0x1p-20f;  // of |lo| + |hi|, rotated: >= 2^-22 (|x| + |y|) twice over
 
 // The least e >= -126 with a <= 448 * 2^e, for finite a >= 0:
 // a = f * 2^k with 1 <= f < 2, and 448 = 1.75 * 2^8.
@@ -35,53 +50,45 @@ __device__ __forceinline__ float to_odd(double v) {
     return ((double)f != v && isfinite(f)) ? __uint_as_float(__float_as_uint(f) | 1u) : f;
 }
 
-template <typename XT>
-__device__ __forceinline__ void load8f(const XT* p, float (&v)[8]) {
-    float a[4], b[4];
-    load4(p, a);
-    load4(p + 4, b);
+__device__ __forceinline__ void load8f(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
 }
-__device__ __forceinline__ void store8(float* p, const double (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = (float)v[i];
+__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const double (&v)[8]) {
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        u[i] = (uint32_t)f32_to_bf16_rn(to_odd(v[2 * i])) | ((uint32_t)f32_to_bf16_rn(to_odd(v[2 * i + 1])) << 16);
+        u[i] = (uint32_t)f32_to_bf16_rn(v[2 * i]) | ((uint32_t)f32_to_bf16_rn(v[2 * i + 1]) << 16);
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// Channels [8l, 8l+8) and [64+8l, 64+8l+8) of one row, rotated to position t.
-template <typename XT>
-__device__ __forceinline__ void load_rotated(const PagedAppendArgs& a, const XT* row, int l, int t, bool rope,
-                                             double (&lo)[8], double (&hi)[8]) {
-    float x[8], y[8];
-    load8f(row + 8 * l, x);
-    load8f(row + kD / 2 + 8 * l, y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo[i] = x[i];
-        hi[i] = y[i];
-        if (rope) {
-            double s, c;
-            sincos((double)t * a.freq[8 * l + i], &s, &c);
-            lo[i] = (double)x[i] * c - (double)y[i] * s;
-            hi[i] = (double)x[i] * s + (double)y[i] * c;
-        }
-    }
+// cos and sin of token t's angle i, rounded to fp32: the angle in turns is
+// reduced to [-1/2, 1/2] in fp64.
+__device__ __forceinline__ float2 turn(int t, double turns_per_token) {
+    const double x = (double)t * turns_per_token;
+    float s, c;
+    sincospif(2.f * (float)(x - rint(x)), &s, &c);
+    return make_float2(c, s);
 }
-
-__device__ __forceinline__ double block_max(double v, double* sh) {
-#pragma unroll
-    for (int m = 16; m; m >>= 1) v = fmax(v, __shfl_xor_sync(kFull, v, m));
-    if (lane_id() == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = fmax(fmax(sh[0], sh[1]), fmax(sh[2], sh[3]));
-    return v;
+// One pair in fp64.
+__device__ __noinline__ double2 exact_pair(float x, float y, int t, double freq) {
+    double s, c;
+    sincos((double)t * freq, &s, &c);
+    return make_double2((double)x * c - (double)y * s, (double)x * s + (double)y * c);
 }
 
 // The item'th page slot that the call writes: sequences in order, each with
@@ -122,120 +129,247 @@ __device__ __forceinline__ bool find_item(const PagedSeqs& s, int page, int64_t 
     return false;
 }
 
-template <typename XT>
-__global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
-    __shared__ double sh[4];
-    const int l = threadIdx.x & 7, rg = threadIdx.x >> 3;
-    const int64_t page_blocks = a.items * 2 * a.Hkv;
-    if (blockIdx.x >= page_blocks) {  // queries: 16 rows of one head
-        const int64_t qb = blockIdx.x - page_blocks;
-        const int64_t r = qb / a.Hq * 16 + rg;
-        const int h = (int)(qb % a.Hq);
-        if (r >= a.seqs.n_rows) return;
-        int t = 0;
-        bool mine = false;
-        for (int b = 0; b < a.seqs.B && !mine; ++b) {
-            const PagedSeq s = paged_seq(a.seqs, b);
-            mine = r >= s.row0 && r < s.row0 + s.rows && s.len >= s.rows;
-            t = s.len - s.rows + (int)(r - s.row0);
-        }
-        if (!mine) return;
-        double lo[8], hi[8];
-        load_rotated(a, reinterpret_cast<const XT*>(a.q) + r * a.q_st + h * a.q_sh, l, t, a.rope != 0, lo, hi);
-        XT* o = reinterpret_cast<XT*>(a.q_out) + (r * a.Hq + h) * kD;
-        store8(o + 8 * l, lo);
-        store8(o + kD / 2 + 8 * l, hi);
-        return;
+// The codes of an older row under a grown scale: old codes are worth `ratio` new ones.
+__device__ __forceinline__ void renew_row(uint8_t* at, double ratio) {
+    const uint2 u = *reinterpret_cast<const uint2*>(at);
+    const uint32_t w[2] = {u.x, u.y};
+    uint32_t n[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t f0 = e4m3x2_to_f16x2(w[i] & 0xffffu), f1 = e4m3x2_to_f16x2(w[i] >> 16);
+        n[i] = e4m3x2(to_odd(f16_lo(f0) * ratio), to_odd(f16_hi(f0) * ratio)) |
+               (e4m3x2(to_odd(f16_lo(f1) * ratio), to_odd(f16_hi(f1) * ratio)) << 16);
+        // NaN codes are kept as they are, sign and all
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (((w[i] >> (8 * k)) & 0x7fu) == 0x7fu) n[i] = (n[i] & ~(0xffu << (8 * k))) | (w[i] & (0xffu << (8 * k)));
     }
-    const int64_t item = blockIdx.x / (2 * a.Hkv);
-    const int hh = (int)(blockIdx.x % (2 * a.Hkv));
+    *reinterpret_cast<uint2*>(at) = make_uint2(n[0], n[1]);
+}
+
+// Block: one page slot (blockIdx.x / groups) and up to `a.heads` heads of K, V
+// or Q (in that order of groups).
+template <typename XT, int PAGE>
+__global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
+    paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+    constexpr int kThreads = AppShape<PAGE>::kThreads, kPasses = AppShape<PAGE>::kPasses, kWarps = kThreads / 32;
+    extern __shared__ float2 cs[];  // [PAGE][64] (cos, sin) of the page's rows
+    __shared__ float top_sh[2][kWarps];
+    __shared__ double top_exact[kWarps];
+    const int l = threadIdx.x & 7, rg = threadIdx.x >> 3, lane = lane_id(), warp = threadIdx.x >> 5;
+    const int gkv = (a.Hkv + a.heads - 1) / a.heads, gq = a.q ? (a.Hq + a.heads - 1) / a.heads : 0;
+    const int64_t item = blockIdx.x / (2 * gkv + gq);
+    int group = (int)(blockIdx.x % (2 * gkv + gq));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && a.seqs.status)
-        for (int b = threadIdx.x; b < a.seqs.B; b += kAppThreads) paged_report(a.seqs, paged_seq(a.seqs, b).bad);
-    const bool is_v = hh >= a.Hkv;
-    const int h = is_v ? hh - a.Hkv : hh;
+        for (int b = threadIdx.x; b < a.seqs.B; b += kThreads) paged_report(a.seqs, paged_seq(a.seqs, b).bad);
     int b = 0, slot = 0;
     PagedSeq seq{};
-    if (!find_item(a.seqs, a.page, item, b, slot, seq)) return;
-    const int64_t id = a.seqs.table[b * a.seqs.table_stride + slot];
-    if (id < 0 || id >= a.num_pages) {
-        if (threadIdx.x == 0 && hh == 0) paged_report(a.seqs, kBadPage);
-        return;
-    }
-    const int start = seq.len - seq.rows;
-    const int first = start > slot * a.page ? start - slot * a.page : 0;  // page row of the first new token
-    const int last = seq.len - slot * a.page < a.page ? seq.len - slot * a.page : a.page;
-    const XT* x = is_v ? reinterpret_cast<const XT*>(a.v) + h * a.v_sh : reinterpret_cast<const XT*>(a.k) + h * a.k_sh;
-    const int64_t st = is_v ? a.v_st : a.k_st;
-    const bool rope = a.rope && !is_v;
-    double top = 0.0;
-    double lo[8], hi[8];
-    for (int r = rg; r < a.page; r += 16) {
-        if (r < first || r >= last) continue;
-        const int t = slot * a.page + r;
-        load_rotated(a, x + (int64_t)(seq.row0 + t - start) * st, l, t, rope, lo, hi);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (isfinite(lo[i])) top = fmax(top, fabs(lo[i]));
-            if (isfinite(hi[i])) top = fmax(top, fabs(hi[i]));
+    if (!find_item(a.seqs, PAGE, item, b, slot, seq)) return;
+    const int kind = group < gkv ? 0 : group < 2 * gkv ? 1 : 2;  // K, V, Q
+    const int h0 = (group - kind * gkv) * a.heads, H = kind == 2 ? a.Hq : a.Hkv;
+    const int h1 = h0 + a.heads < H ? h0 + a.heads : H;
+    const int start = seq.len - seq.rows, t0 = slot * PAGE;
+    const int first = start > t0 ? start - t0 : 0;  // page row of the first new token
+    const int last = seq.len - t0 < PAGE ? seq.len - t0 : PAGE;
+    int64_t id = 0;
+    if (kind < 2) {
+        id = a.seqs.table[b * a.seqs.table_stride + slot];
+        if (id < 0 || id >= a.num_pages) {
+            if (threadIdx.x == 0) paged_report(a.seqs, kBadPage);
+            return;
         }
     }
-    top = block_max(top, sh);
-    float* scale = (is_v ? a.vs : a.ks) + id * a.Hkv + h;
-    uint8_t* codes = (is_v ? a.vc : a.kc) + (id * a.Hkv + h) * (int64_t)a.page * kD;
-    double s_new = exp2i(cover_exponent(top));
-    double ratio = 1.0;  // old codes are worth ratio new ones
-    if (first > 0) {
-        const float old = *scale;
-        if (old > 0.f && isfinite(old)) {
-            if (top <= 448.0 * (double)old) s_new = (double)old;
-            else ratio = (double)old / s_new;
-        }
+    const bool rope = a.rope && kind != 1;
+    if (rope) {
+        for (int i = threadIdx.x; i < (last - first) * 64; i += kThreads)
+            cs[(first + (i >> 6)) * 64 + (i & 63)] = turn(t0 + first + (i >> 6), a.turns[i & 63]);
+        __syncthreads();
     }
-    __syncthreads();  // every thread has read the old scale
-    if (threadIdx.x == 0) *scale = (float)s_new;
-    const double inv = 1.0 / s_new;
-    for (int r = rg; r < last; r += 16) {
-        uint8_t* dst = codes + r * kD;
-        if (r < first) {
-            if (ratio == 1.0) continue;
+    const int64_t st = kind == 0 ? a.k_st : kind == 1 ? a.v_st : a.q_st;
+    const int64_t sh = kind == 0 ? a.k_sh : kind == 1 ? a.v_sh : a.q_sh;
+    const XT* x0 = reinterpret_cast<const XT*>(kind == 0 ? a.k : kind == 1 ? a.v : a.q);
+    const int64_t row0 = seq.row0 + t0 - start;  // packed row of page row 0
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h) {
+        const XT* x = x0 + h * sh;
+        float lo[kPasses][8], hi[kPasses][8];
+        float top = 0.f;
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                uint2 u = *reinterpret_cast<const uint2*>(dst + p * (kD / 2) + 8 * l);
-                uint32_t w[2] = {u.x, u.y}, n[2];
+        for (int p = 0; p < kPasses; ++p) {
+            const int r = rg + p * (kThreads / 8);
+            if (r >= first && r < last) {
+                const XT* row = x + (row0 + r) * st;
+                load8f(row + 8 * l, lo[p]);
+                load8f(row + kD / 2 + 8 * l, hi[p]);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t f0 = e4m3x2_to_f16x2(w[i] & 0xffffu), f1 = e4m3x2_to_f16x2(w[i] >> 16);
-                    n[i] = e4m3x2(to_odd(f16_lo(f0) * ratio), to_odd(f16_hi(f0) * ratio)) |
-                           (e4m3x2(to_odd(f16_lo(f1) * ratio), to_odd(f16_hi(f1) * ratio)) << 16);
+                for (int i = 0; i < 8; ++i) lo[p][i] = hi[p][i] = 0.f;
+            }
+        }
+        if (rope) {
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) {
+                const int r = rg + p * (kThreads / 8);
+                if (r < first || r >= last) continue;
+                const float4* t = reinterpret_cast<const float4*>(cs + r * 64 + 8 * l);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float4 w = t[i >> 1];
+                    const float x0 = lo[p][i], y0 = hi[p][i], x1 = lo[p][i + 1], y1 = hi[p][i + 1];
+                    lo[p][i] = fmaf(x0, w.x, -(y0 * w.y));
+                    hi[p][i] = fmaf(x0, w.y, y0 * w.x);
+                    lo[p][i + 1] = fmaf(x1, w.z, -(y1 * w.w));
+                    hi[p][i + 1] = fmaf(x1, w.w, y1 * w.z);
                 }
-                *reinterpret_cast<uint2*>(dst + p * (kD / 2) + 8 * l) = make_uint2(n[0], n[1]);
+            }
+        }
+        if (kind == 2) {
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) {
+                const int r = rg + p * (kThreads / 8);
+                if (r < first || r >= last) continue;
+                XT* o = reinterpret_cast<XT*>(a.q_out) + ((row0 + r) * a.Hq + h) * kD;
+                store8(o + 8 * l, lo[p]);
+                store8(o + kD / 2 + 8 * l, hi[p]);
             }
             continue;
         }
-        const int t = slot * a.page + r;
-        load_rotated(a, x + (int64_t)(seq.row0 + t - start) * st, l, t, rope, lo, hi);
-        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            w[i] = e4m3x2(to_odd(lo[4 * i] * inv), to_odd(lo[4 * i + 1] * inv)) |
-                   (e4m3x2(to_odd(lo[4 * i + 2] * inv), to_odd(lo[4 * i + 3] * inv)) << 16);
-            w[2 + i] = e4m3x2(to_odd(hi[4 * i] * inv), to_odd(hi[4 * i + 1] * inv)) |
-                       (e4m3x2(to_odd(hi[4 * i + 2] * inv), to_odd(hi[4 * i + 3] * inv)) << 16);
+        for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // Infinities and NaN do not count; rotated in fp32, they may stand for a
+                // finite value: such a page is decided in fp64 (top = infinity).
+                const float u = fabsf(lo[p][i]), v = fabsf(hi[p][i]), none = rope ? INFINITY : 0.f;
+                top = fmaxf(top, u < INFINITY ? u : none);
+                top = fmaxf(top, v < INFINITY ? v : none);
+            }
+        top = warp_max(top);
+        if (lane == 0) top_sh[h & 1][warp] = top;
+        float* scale = (kind ? a.vs : a.ks) + id * a.Hkv + h;
+        uint8_t* codes = (kind ? a.vc : a.kc) + (id * a.Hkv + h) * (int64_t)(PAGE * kD);
+        const float old = first > 0 ? *scale : 0.f;
+        const bool had = old > 0.f && old < INFINITY;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, top_sh[h & 1][w]);
+        int e = cover_exponent(top < INFINITY ? top : 0.f);
+        bool keep = had && (double)top <= 448.0 * (double)old;
+        if (rope) {
+            const double up = (double)top * (1.0 + (double)kErr), down = (double)top * (1.0 - (double)kErr);
+            if (!(top < INFINITY) || cover_exponent(up) != cover_exponent(down) ||
+                (had && (up <= 448.0 * (double)old) != (down <= 448.0 * (double)old))) {  // the whole block decides alike
+                double most = 0.0;
+#pragma unroll 1
+                for (int r = rg; r < last; r += kThreads / 8) {
+                    if (r < first) continue;
+#pragma unroll 1
+                    for (int i = 8 * l; i < 8 * l + 8; ++i) {
+                        const XT* row = x + (row0 + r) * st;
+                        const double2 v = exact_pair((float)row[i], (float)row[kD / 2 + i], t0 + r, a.freq[i]);
+                        if (isfinite(v.x)) most = fmax(most, fabs(v.x));
+                        if (isfinite(v.y)) most = fmax(most, fabs(v.y));
+                    }
+                }
+#pragma unroll
+                for (int m = 16; m; m >>= 1) most = fmax(most, __shfl_xor_sync(kFull, most, m));
+                if (lane == 0) top_exact[warp] = most;
+                __syncthreads();
+                for (int w = 0; w < kWarps; ++w) most = fmax(most, top_exact[w]);
+                __syncthreads();
+                e = cover_exponent(most);
+                keep = had && most <= 448.0 * (double)old;
+            }
         }
-        *reinterpret_cast<uint2*>(dst + 8 * l) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2*>(dst + kD / 2 + 8 * l) = make_uint2(w[2], w[3]);
+        const double s_new = keep ? (double)old : exp2i(e);
+        if (threadIdx.x == 0) *scale = (float)s_new;
+        const double ratio = keep || !had ? 1.0 : (double)old / s_new;
+        const double inv_d = 1.0 / s_new;
+        const float inv = (float)inv_d;
+        const float tiny = 0x1p-148f * inv;  // what rounding among fp32's subnormal values adds
+        // a scale that is no power of two (a caller's own) has a rounded inverse
+        const bool unsure = rope || (double)inv != inv_d || (__float_as_uint((float)s_new) & 0x7fffffu) != 0;
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const int r = rg + p * (kThreads / 8);
+            if (r >= last) continue;
+            uint8_t* dst = codes + r * kD + 8 * l;
+            if (r < first) {
+                if (ratio != 1.0) {
+                    renew_row(dst, ratio);
+                    renew_row(dst + kD / 2, ratio);
+                }
+                continue;
+            }
+            uint32_t w[4] = {0, 0, 0, 0}, odd = 0;  // odd: channels (16 of them) whose code is not sure
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float u0 = lo[p][i] * inv, u1 = lo[p][i + 1] * inv, v0 = hi[p][i] * inv, v1 = hi[p][i + 1] * inv;
+                uint32_t cu, cv;
+                if (unsure) {
+                    const float d0 = fmaf(fabsf(u0) + fabsf(v0), kErr, tiny), d1 = fmaf(fabsf(u1) + fabsf(v1), kErr, tiny);
+                    cu = e4m3x2(u0 - d0, u1 - d1);
+                    cv = e4m3x2(v0 - d0, v1 - d1);
+                    const uint32_t xu = cu ^ e4m3x2(u0 + d0, u1 + d1), xv = cv ^ e4m3x2(v0 + d0, v1 + d1);
+                    odd |= ((xu & 0xffu ? 1u : 0u) | (xu >> 8 ? 2u : 0u) | (xv & 0xffu ? 256u : 0u) | (xv >> 8 ? 512u : 0u)) << i;
+                } else {
+                    cu = e4m3x2(u0, u1);
+                    cv = e4m3x2(v0, v1);
+                }
+                w[i >> 2] |= cu << ((i & 2) * 8);
+                w[2 + (i >> 2)] |= cv << ((i & 2) * 8);
+            }
+#pragma unroll 1
+            for (; odd; odd &= odd - 1) {
+                const int k = __ffs(odd) - 1, i = 8 * l + (k & 7);
+                const XT* row = x + (row0 + r) * st;
+                const float xa = (float)row[i], xb = (float)row[kD / 2 + i];
+                double2 v = make_double2(xa, xb);
+                if (rope) v = exact_pair(xa, xb, t0 + r, a.freq[i]);
+                const uint32_t c = e4m3x2(to_odd((k < 8 ? v.x : v.y) * inv_d), 0.f) & 0xffu;
+                const int at = (k & 3) * 8;
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (m == (k >> 3) * 2 + ((k & 7) >> 2)) w[m] = (w[m] & ~(0xffu << at)) | (c << at);
+            }
+            *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2*>(dst + kD / 2) = make_uint2(w[2], w[3]);
+        }
+    }
+}
+
+template <typename XT, int PAGE>
+cudaError_t launch_page(const PagedAppendArgs& a, int64_t grid, cudaStream_t s) {
+    static std::atomic<unsigned long long> ready{0};
+    return launch_smem_pdl(paged_append_kernel<XT, PAGE>, ready, dim3((unsigned)grid), dim3(AppShape<PAGE>::kThreads),
+                           a.rope ? PAGE * 64 * sizeof(float2) : 0, s, a);
+}
+template <typename XT>
+cudaError_t launch_type(const PagedAppendArgs& a, int64_t grid, cudaStream_t s) {
+    switch (a.page) {
+        case 16: return launch_page<XT, 16>(a, grid, s);
+        case 32: return launch_page<XT, 32>(a, grid, s);
+        case 64: return launch_page<XT, 64>(a, grid, s);
+        default: return launch_page<XT, 128>(a, grid, s);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_append(const PagedAppendArgs& a, bool bf16, cudaStream_t s) {
-    const int64_t qblocks = a.q ? (a.seqs.n_rows + 15) / 16 * a.Hq : 0;
-    const int64_t grid = a.items * 2 * a.Hkv + qblocks;
+cudaError_t launch_paged_append(PagedAppendArgs a, bool bf16, cudaStream_t s) {
+    // Heads per block: more of them share a page's cos and sin (computing those
+    // costs a block as much as two or three heads), as long as there are blocks
+    // for every SM eight times over.
+    int64_t grid = 0;
+    for (a.heads = 8;; a.heads /= 2) {
+        const int64_t kv = (a.Hkv + a.heads - 1) / a.heads, q = a.q ? (a.Hq + a.heads - 1) / a.heads : 0;
+        grid = a.items * (2 * kv + q);
+        if (a.heads == 1 || grid >= 8 * (int64_t)device_sm_count()) break;
+    }
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    if (bf16) paged_append_kernel<__nv_bfloat16><<<(unsigned)grid, kAppThreads, 0, s>>>(a);
-    else paged_append_kernel<float><<<(unsigned)grid, kAppThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return bf16 ? launch_type<__nv_bfloat16>(a, grid, s) : launch_type<float>(a, grid, s);
 }
 
 }  // namespace nsnq
