@@ -26,8 +26,8 @@ namespace {
 // rotation's pairs). A thread takes kPasses rows of a page.
 template <int PAGE>
 struct AppShape {
-    static constexpr int kThreads = PAGE == 128 ? 256 : 128;
-    static constexpr int kPasses = PAGE * 8 / kThreads;
+    static constexpr int kPasses = PAGE == 16 ? 1 : 2;
+    static constexpr int kThreads = PAGE * 8 / kPasses;
 };
 constexpr float kErr = 0x1p-20f;  // of |lo| + |hi|, rotated: >= 2^-22 (|x| + |y|) twice over
 
@@ -50,20 +50,36 @@ __device__ __forceinline__ float to_odd(double v) {
     return ((double)f != v && isfinite(f)) ? __uint_as_float(__float_as_uint(f) | 1u) : f;
 }
 
-__device__ __forceinline__ void load8f(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight channels as they lie in memory, and as fp32.
+template <typename XT>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
     }
-}
-__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -71,8 +87,7 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        u[i] = (uint32_t)f32_to_bf16_rn(v[2 * i]) | ((uint32_t)f32_to_bf16_rn(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
@@ -182,15 +197,31 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
         }
     }
     const bool rope = a.rope && kind != 1;
+    const int64_t st = kind == 0 ? a.k_st : kind == 1 ? a.v_st : a.q_st;
+    const int64_t sh = kind == 0 ? a.k_sh : kind == 1 ? a.v_sh : a.q_sh;
+    const XT* x0 = reinterpret_cast<const XT*>(kind == 0 ? a.k : kind == 1 ? a.v : a.q);
+    const int64_t row0 = seq.row0 + t0 - start;  // packed row of page row 0
+    Raw8<XT> raw[kPasses][2];  // of the next head: its loads run under this one's work
+    auto fetch = [&](int h) {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const int r = rg + p * (kThreads / 8);
+            if (r >= first && r < last) {
+                const XT* row = x0 + h * sh + (row0 + r) * st;
+                raw[p][0].load(row + 8 * l);
+                raw[p][1].load(row + kD / 2 + 8 * l);
+            } else {
+                raw[p][0].zero();
+                raw[p][1].zero();
+            }
+        }
+    };
+    fetch(h0);
     if (rope) {
         for (int i = threadIdx.x; i < (last - first) * 64; i += kThreads)
             cs[(first + (i >> 6)) * 64 + (i & 63)] = turn(t0 + first + (i >> 6), a.turns[i & 63]);
         __syncthreads();
     }
-    const int64_t st = kind == 0 ? a.k_st : kind == 1 ? a.v_st : a.q_st;
-    const int64_t sh = kind == 0 ? a.k_sh : kind == 1 ? a.v_sh : a.q_sh;
-    const XT* x0 = reinterpret_cast<const XT*>(kind == 0 ? a.k : kind == 1 ? a.v : a.q);
-    const int64_t row0 = seq.row0 + t0 - start;  // packed row of page row 0
 #pragma unroll 1
     for (int h = h0; h < h1; ++h) {
         const XT* x = x0 + h * sh;
@@ -198,16 +229,11 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
         float top = 0.f;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-            const int r = rg + p * (kThreads / 8);
-            if (r >= first && r < last) {
-                const XT* row = x + (row0 + r) * st;
-                load8f(row + 8 * l, lo[p]);
-                load8f(row + kD / 2 + 8 * l, hi[p]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) lo[p][i] = hi[p][i] = 0.f;
-            }
+            raw[p][0].get(lo[p]);
+            raw[p][1].get(hi[p]);
         }
+        // (q_out may be q: a head's own rows are read before any is written)
+        if (h + 1 < h1) fetch(h + 1);
         if (rope) {
 #pragma unroll
             for (int p = 0; p < kPasses; ++p) {
