@@ -29,6 +29,9 @@ struct AppShape {
     static constexpr int kPasses = PAGE == 16 ? 1 : 2;
     static constexpr int kThreads = PAGE * 8 / kPasses;
 };
+// Heads whose rows a block has on their way or at hand.
+template <typename XT>
+constexpr int app_ahead() { return sizeof(XT) == 2 ? 3 : 2; }
 constexpr float kErr = 0x1p-20f;  // of |lo| + |hi|, rotated: >= 2^-22 (|x| + |y|) twice over
 
 // The least e >= -126 with a <= 448 * 2^e, for finite a >= 0:
@@ -50,36 +53,30 @@ __device__ __forceinline__ float to_odd(double v) {
     return ((double)f != v && isfinite(f)) ? __uint_as_float(__float_as_uint(f) | 1u) : f;
 }
 
-// Eight channels as they lie in memory, and as fp32.
-template <typename XT>
-struct Raw8;
-template <>
-struct Raw8<__nv_bfloat16> {
-    uint4 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void load8f(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-};
-template <>
-struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = __ldcs(reinterpret_cast<const float4*>(p));
-        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-};
+}
+__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+// Eight channels to shared memory, asynchronously.
+template <typename XT>
+__device__ __forceinline__ void copy8(XT* dst, const XT* src) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(XT) / 2; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(dst) + 16 * i),
+                     "l"(reinterpret_cast<const char*>(src) + 16 * i)
+                     : "memory");
+}
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -168,7 +165,8 @@ template <typename XT, int PAGE>
 __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
     paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
     constexpr int kThreads = AppShape<PAGE>::kThreads, kPasses = AppShape<PAGE>::kPasses, kWarps = kThreads / 32;
-    extern __shared__ float2 cs[];  // [PAGE][64] (cos, sin) of the page's rows
+    constexpr int kAhead = app_ahead<XT>();
+    extern __shared__ __align__(16) float2 cs[];  // [PAGE][64] (cos, sin) of the page's rows, then the heads' rows
     __shared__ float top_sh[2][kWarps];
     __shared__ double top_exact[kWarps];
     const int l = threadIdx.x & 7, rg = threadIdx.x >> 3, lane = lane_id(), warp = threadIdx.x >> 5;
@@ -201,22 +199,25 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
     const int64_t sh = kind == 0 ? a.k_sh : kind == 1 ? a.v_sh : a.q_sh;
     const XT* x0 = reinterpret_cast<const XT*>(kind == 0 ? a.k : kind == 1 ? a.v : a.q);
     const int64_t row0 = seq.row0 + t0 - start;  // packed row of page row 0
-    Raw8<XT> raw[kPasses][2];  // of the next head: its loads run under this one's work
+    // The rows of the next heads are on their way to shared memory; a thread
+    // reads only what it copied itself.
+    XT* ring = reinterpret_cast<XT*>(cs + (a.rope ? PAGE * 64 : 0));
     auto fetch = [&](int h) {
+        if (h < h1) {
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            const int r = rg + p * (kThreads / 8);
-            if (r >= first && r < last) {
-                const XT* row = x0 + h * sh + (row0 + r) * st;
-                raw[p][0].load(row + 8 * l);
-                raw[p][1].load(row + kD / 2 + 8 * l);
-            } else {
-                raw[p][0].zero();
-                raw[p][1].zero();
+            for (int p = 0; p < kPasses; ++p) {
+                const int r = rg + p * (kThreads / 8);
+                if (r < first || r >= last) continue;
+                const XT* row = x0 + h * sh + (row0 + r) * st + 8 * l;
+                XT* to = ring + (((h - h0) % kAhead) * PAGE + r) * kD + 8 * l;
+                copy8(to, row);
+                copy8(to + kD / 2, row + kD / 2);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(h0);
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) fetch(h0 + i);
     if (rope) {
         for (int i = threadIdx.x; i < (last - first) * 64; i += kThreads)
             cs[(first + (i >> 6)) * 64 + (i & 63)] = turn(t0 + first + (i >> 6), a.turns[i & 63]);
@@ -227,13 +228,21 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
         const XT* x = x0 + h * sh;
         float lo[kPasses][8], hi[kPasses][8];
         float top = 0.f;
+        // (q_out may be q: a head's rows are all read before one of them is written)
+        fetch(h + kAhead - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-            raw[p][0].get(lo[p]);
-            raw[p][1].get(hi[p]);
+            const int r = rg + p * (kThreads / 8);
+            if (r >= first && r < last) {
+                const XT* from = ring + (((h - h0) % kAhead) * PAGE + r) * kD + 8 * l;
+                load8f(from, lo[p]);
+                load8f(from + kD / 2, hi[p]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) lo[p][i] = hi[p][i] = 0.f;
+            }
         }
-        // (q_out may be q: a head's own rows are read before any is written)
-        if (h + 1 < h1) fetch(h + 1);
         if (rope) {
 #pragma unroll
             for (int p = 0; p < kPasses; ++p) {
@@ -370,7 +379,7 @@ template <typename XT, int PAGE>
 cudaError_t launch_page(const PagedAppendArgs& a, int64_t grid, cudaStream_t s) {
     static std::atomic<unsigned long long> ready{0};
     return launch_smem_pdl(paged_append_kernel<XT, PAGE>, ready, dim3((unsigned)grid), dim3(AppShape<PAGE>::kThreads),
-                           a.rope ? PAGE * 64 * sizeof(float2) : 0, s, a);
+                           (a.rope ? PAGE * 64 * sizeof(float2) : 0) + app_ahead<XT>() * PAGE * kD * sizeof(XT), s, a);
 }
 template <typename XT>
 cudaError_t launch_type(const PagedAppendArgs& a, int64_t grid, cudaStream_t s) {
@@ -389,7 +398,7 @@ cudaError_t launch_paged_append(PagedAppendArgs a, bool bf16, cudaStream_t s) {
     // costs a block as much as two or three heads), as long as there are blocks
     // for every SM eight times over.
     int64_t grid = 0;
-    for (a.heads = 8;; a.heads /= 2) {
+    for (a.heads = 32;; a.heads /= 2) {
         const int64_t kv = (a.Hkv + a.heads - 1) / a.heads, q = a.q ? (a.Hq + a.heads - 1) / a.heads : 0;
         grid = a.items * (2 * kv + q);
         if (a.heads == 1 || grid >= 8 * (int64_t)device_sm_count()) break;
