@@ -30,7 +30,6 @@ of a call packed, the last tokens of their sequences):
 from __future__ import annotations
 
 import collections
-import contextlib
 import ctypes
 import dataclasses
 import os
@@ -645,37 +644,45 @@ class PagedCache:
         return c
 
 
-def _paged_seqs(dev, B, n_rows, page_table, seq_lens, cu_rows):
-    """Checks of the device arrays that describe a call's sequences."""
-    for name, t, dim in (("page_table", page_table, 2), ("seq_lens", seq_lens, 1), ("cu_rows", cu_rows, 1)):
-        if t is None:
-            continue
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32")
-        if t.dim() != dim or t.device != dev or (t.numel() and t.stride(dim - 1) != 1):
-            raise ValueError(f"{name} must be a {dim}-dimensional tensor on {dev} with contiguous rows")
-    if page_table.shape[0] != B:
-        raise ValueError(f"page_table has {page_table.shape[0]} rows for {B} sequences")
+def _paged_seqs(dev, n_rows, page_table, seq_lens, cu_rows):
+    """Checks of the device arrays that describe a call's sequences; returns
+    (sequences, table columns, table row stride, cu_rows' address)."""
+    i32 = torch.int32
+    if page_table.dtype is not i32 or seq_lens.dtype is not i32 or (cu_rows is not None and cu_rows.dtype is not i32):
+        raise TypeError("page_table, seq_lens and cu_rows must be int32")
+    if seq_lens.dim() != 1 or page_table.dim() != 2 or seq_lens.device != dev or page_table.device != dev:
+        raise ValueError(f"seq_lens must be [B] and page_table [B][columns], on {dev}")
+    B = seq_lens.shape[0]
+    rows, cols = page_table.shape
+    stride, step = page_table.stride()
+    if rows != B:
+        raise ValueError(f"page_table has {rows} rows for {B} sequences")
+    if (cols > 1 and step != 1) or (B > 1 and seq_lens.stride(0) != 1):
+        raise ValueError("seq_lens and the rows of page_table must be contiguous")
     if cu_rows is None:
         if n_rows != B:
             raise ValueError(f"{n_rows} rows for {B} sequences: pass cu_rows")
-    elif cu_rows.shape[0] != B + 1:
-        raise ValueError(f"cu_rows must hold {B + 1} entries")
+        return B, cols, max(stride, cols), None
+    if cu_rows.dim() != 1 or cu_rows.shape[0] != B + 1 or cu_rows.device != dev or (B and cu_rows.stride(0) != 1):
+        raise ValueError(f"cu_rows must hold {B + 1} contiguous entries on {dev}")
+    return B, cols, max(stride, cols), cu_rows.data_ptr()
 
 
-class _OnStream:
-    """The device of a call's tensors made current, and its stream with it, so
-    that what the call allocates belongs to the stream that uses it."""
-
-    def __new__(cls, device, stream):
-        if stream is None:
-            return contextlib.nullcontext() if device.index == torch.cuda.current_device() \
-                else torch.cuda.device(device)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream)
+def _on_stream(dev, stream, call):
+    """call(raw stream) with the device of its tensors current and, with it, the
+    given stream, so that what the call allocates belongs to the stream that
+    uses it."""
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(dev):
+            return call(torch.cuda.current_stream().cuda_stream)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def nsnq_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
@@ -688,31 +695,34 @@ def nsnq_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, page_
     tokens: seq_lens[b] counts its tokens with them. page_table [B][columns]
     lists each sequence's pages. With q [rows][Hq][D], returns q rotated the
     same way (into q_out if given)."""
-    N, H, D = k.shape
-    c, dev, B = cache._c(), k.device, int(seq_lens.shape[0])
-    if v.shape != k.shape or v.dtype != k.dtype or k.stride(2) != 1 or v.stride(2) != 1:
+    c, dev, dtype = cache._c(), k.device, k.dtype
+    N, H, D = shape = k.shape
+    ks, vs = k.stride(), v.stride()
+    if v.shape != shape or v.dtype is not dtype or ks[2] != 1 or vs[2] != 1:
         raise ValueError("k and v must have the same shape and dtype and contiguous channels")
     if dev != cache.k.device or v.device != dev:
         raise ValueError("k, v and the cache must be on one device")
-    _paged_seqs(dev, B, N, page_table, seq_lens, cu_rows)
-    Hq, qs = H, (0, 0)
-    with _OnStream(dev, stream):
-        if q is not None:
-            if q.dim() != 3 or q.shape[0] != N or q.shape[2] != D or q.dtype != k.dtype or q.stride(2) != 1 \
-                    or q.device != dev:
-                raise ValueError("q must be [rows][Hq][D] like k, with contiguous channels")
-            Hq, qs = int(q.shape[1]), q.stride()
-            if q_out is None:
-                q_out = torch.empty(N, Hq, D, dtype=q.dtype, device=dev)
-            elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous() \
-                    or q_out.device != dev:
-                raise ValueError("q_out must be contiguous, of q's shape and dtype")
-        _check(load().nsnq_paged_append(_ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _dtype_code(k), N,
-                                        k.stride(0), k.stride(1), v.stride(0), v.stride(1), qs[0], qs[1],
-                                        _ptr(cu_rows), _ptr(seq_lens), B, Hq, H, D, float(rope_base), c,
-                                        _ptr(page_table), page_table.shape[1],
-                                        max(page_table.stride(0), page_table.shape[1]), _stream(stream)))
-    return q_out if q is not None else None
+    B, cols, stride, cu = _paged_seqs(dev, N, page_table, seq_lens, cu_rows)
+    if q is None:
+        q_out, Hq, qs, qp = None, H, (0, 0), None
+    else:
+        qn, Hq, qd = q_shape = q.shape
+        qs, qp = q.stride(), q.data_ptr()
+        if qn != N or qd != D or q.dtype is not dtype or qs[2] != 1 or q.device != dev:
+            raise ValueError("q must be [rows][Hq][D] like k, with contiguous channels")
+        if q_out is not None and (q_out.shape != q_shape or q_out.dtype is not dtype or q_out.device != dev
+                                  or not q_out.is_contiguous()):
+            raise ValueError("q_out must be contiguous, of q's shape and dtype")
+
+    def call(raw):
+        out = torch.empty(q_shape, dtype=dtype, device=dev) if q is not None and q_out is None else q_out
+        _check(load().nsnq_paged_append(k.data_ptr(), v.data_ptr(), qp, None if out is None else out.data_ptr(),
+                                        _dtype_code(k), N, ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], cu,
+                                        seq_lens.data_ptr(), B, Hq, H, D, rope_base, c, page_table.data_ptr(),
+                                        cols, stride, raw))
+        return out
+
+    return _on_stream(dev, stream, call)
 
 
 def nsnq_paged_attn_workspace(n_rows: int, B: int, Hq: int, Hkv: int, max_rows: int, D: int = HEAD_DIM) -> int:
@@ -728,24 +738,26 @@ def nsnq_paged_attn(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     the last tokens of their sequences, over the paged cache: returns
     [rows][Hq][D]. max_rows bounds the rows of a sequence. With window > 0 a
     row sees the last `window` tokens up to its own and the first `sinks`."""
-    N, Hq, D = q.shape
-    c, dev, B = cache._c(), q.device, int(seq_lens.shape[0])
-    if q.stride(2) != 1 or dev != cache.k.device:
+    c, dev = cache._c(), q.device
+    N, Hq, D = shape = q.shape
+    qs = q.stride()
+    if qs[2] != 1 or dev != cache.k.device:
         raise ValueError("q must have contiguous channels and be on the cache's device")
-    _paged_seqs(dev, B, N, page_table, seq_lens, cu_rows)
-    with _OnStream(dev, stream):
-        if out is None:
-            out = torch.empty(N, Hq, D, dtype=out_dtype, device=dev)
-        elif out.shape != q.shape or not out.is_contiguous() or out.device != dev:
-            raise ValueError("out must be contiguous, of q's shape")
-        if workspace is None:
-            workspace = _workspace(nsnq_paged_attn_workspace(N, B, Hq, cache.heads, max_rows, D), dev)
-        elif workspace.device != dev:
-            raise ValueError("the workspace must be on the cache's device")
-        _check(load().nsnq_paged_attn(_ptr(q), _dtype_code(q), N, q.stride(0), q.stride(1), _ptr(cu_rows),
-                                      max_rows, _ptr(seq_lens), B, Hq, cache.heads, D, c,
-                                      _ptr(page_table), page_table.shape[1],
-                                      max(page_table.stride(0), page_table.shape[1]), window, sinks,
-                                      float(softmax_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream(stream)))
-    return out
+    B, cols, stride, cu = _paged_seqs(dev, N, page_table, seq_lens, cu_rows)
+    if out is not None and (out.shape != shape or out.device != dev or not out.is_contiguous()):
+        raise ValueError("out must be contiguous, of q's shape")
+    if workspace is not None and workspace.device != dev:
+        raise ValueError("the workspace must be on the cache's device")
+
+    def call(raw):
+        to = torch.empty(shape, dtype=out_dtype, device=dev) if out is None else out
+        ws = workspace
+        if ws is None:
+            ws = _workspace(nsnq_paged_attn_workspace(N, B, Hq, c.heads, max_rows, D), dev)
+        _check(load().nsnq_paged_attn(q.data_ptr(), _dtype_code(q), N, qs[0], qs[1], cu, max_rows,
+                                      seq_lens.data_ptr(), B, Hq, c.heads, D, c, page_table.data_ptr(), cols,
+                                      stride, window, sinks, softmax_scale, to.data_ptr(), _dtype_code(to),
+                                      ws.data_ptr(), ws.nbytes, raw))
+        return to
+
+    return _on_stream(dev, stream, call)
