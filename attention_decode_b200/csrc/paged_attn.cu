@@ -7,7 +7,7 @@
 // can run at the rate of the memory. What meets the codes has to be e4m3
 // too: a query row and a column of weights are each split into pieces of 4
 // significant bits,
-//   x = sum_k 2^(-5k) e4m3(2^(5k) (x - pieces before)),
+//   x = sum_k 2^(-gk) e4m3(2^(gk) (x - pieces before)),  g = 5 or 6,
 // and every piece is a column of its own. The scores of a tile are
 //   S[token][piece, row] = K q^T   (M = 128 tokens, N = pieces x rows, K = 128 channels),
 // lane t of TMEM holding token t; a thread adds its token's pieces, applies
@@ -22,7 +22,7 @@
 // The running maximum m of a row may lag by 2^kLag, so that a tile seldom
 // needs it raised: a vote of the 128 token threads per tile decides; sums of
 // p stay per thread until the segment ends. The bias 2^kBias keeps the
-// smallest piece of a weight at 2^-25 of the row's largest weight.
+// smallest piece of a weight at 2^-24 of the row's largest weight.
 #include <math.h>
 
 #include "attn_split.cuh"
@@ -33,7 +33,8 @@ namespace nsnq {
 namespace {
 
 constexpr int kThreads = 192;  // warps 0-3: tokens / channels; 4: TMA; 5: MMA issue
-constexpr float kLag = 3.f, kBias = 5.f;
+constexpr float kLag = 5.f, kBias = 2.f;  // weights stay below 2^7 (1 + 2^-20)
+constexpr int kShift = 6;                  // bits between the pieces of a weight
 constexpr int kMaxSlots = 8;   // pages per tile (page_size 16)
 constexpr int kSetup = 1;      // tiles that a unit's queries and epilogue cost
 
@@ -57,7 +58,7 @@ struct Misc {
     PagedRange range;
     uint32_t ok[3];               // stage: pages of the tile that were loaded
     float ks[3][kMaxSlots], vs[3][kMaxSlots];
-    float c[32];                  // row: score scale (softmax scale, log2 e, query scale)
+    float2 cb[32];                // row: score scale (softmax scale, log2 e, query scale); bias - maximum
     float m[32];                  // row: running maximum (log2 units)
     int pos[32];                  // row: token position
     float red[4][33];
@@ -74,9 +75,9 @@ __device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
     return r;
 }
-__device__ __forceinline__ uint32_t f16x2_rest(uint32_t h, uint32_t c) {  // (h - c) * 32, exact
+__device__ __forceinline__ uint32_t f16x2_rest(uint32_t h, uint32_t c) {  // (h - c) * 2^kShift, exact
     uint32_t r;
-    asm("{.reg .b32 d;\n\tsub.f16x2 d, %1, %2;\n\tmul.f16x2 %0, d, %3;}" : "=r"(r) : "r"(h), "r"(c), "r"(0x50005000u));
+    asm("{.reg .b32 d;\n\tsub.f16x2 d, %1, %2;\n\tmul.f16x2 %0, d, %3;}" : "=r"(r) : "r"(h), "r"(c), "r"(0x54005400u));
     return r;
 }
 
@@ -95,8 +96,8 @@ __device__ __forceinline__ void weight_pieces(float w0, float w1, uint32_t (&out
         for (int k = 0; k < PP; ++k) {
             out[k] = e4m3x2(w0, w1);
             const uint32_t h = e4m3x2_to_f16x2(out[k]);
-            w0 = (w0 - f16_lo(h)) * 32.f;
-            w1 = (w1 - f16_hi(h)) * 32.f;
+            w0 = (w0 - f16_lo(h)) * (float)(1 << kShift);
+            w1 = (w1 - f16_hi(h)) * (float)(1 << kShift);
         }
     }
 }
@@ -111,6 +112,31 @@ __device__ __forceinline__ bool any_token(bool v) {  // vote of the 128 token th
         : "r"((uint32_t)v)
         : "memory");
     return r != 0;
+}
+
+// Scores of this thread's token: the pieces of each row added up, under the
+// token's k scale (not yet the row's).
+template <int RC, int QP>
+__device__ __forceinline__ void row_scores(uint32_t s, float ks, float (&y)[RC]) {
+    constexpr int W = RC * QP % 32 == 0 ? 32 : RC * QP % 16 == 0 ? 16 : 8;  // columns a load
+#pragma unroll
+    for (int c0 = 0; c0 < RC * QP; c0 += W) {
+        float v[W];
+        tmem_ld<W>(s + c0, v);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int k = (c0 + i) / RC, r = (c0 + i) % RC;
+            y[r] = k == 0 ? v[i] : fmaf(v[i], 1.f / (float)(1ull << (5 * k)), y[r]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RC; ++r) y[r] *= ks;
+}
+
+__device__ __forceinline__ float warp_max_f32(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 template <int RC, int QP, typename QT>
@@ -156,7 +182,7 @@ __device__ __forceinline__ void write_queries(const PagedAttnArgs& a, const Page
             *reinterpret_cast<uint32_t*>(q_sm + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4) = word;
         }
         if (lane == 0) {
-            ms.c[r] = a.scale_log2 * down;
+            ms.cb[r] = make_float2(a.scale_log2 * down, r < u.rows ? INFINITY : kBias);
             ms.pos[r] = pos;
             ms.m[r] = r < u.rows ? -INFINITY : 0.f;
 #pragma unroll
@@ -337,29 +363,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 wait(smem_u32(&ms.s_full[buf]), (it >> 1) & 1);
                 wait(smem_u32(&ms.full[st]), (it / ST) & 1);
                 tc_fence_after();
-                float y[RC];
-#pragma unroll
-                for (int r = 0; r < RC; ++r) y[r] = 0.f;
-                constexpr int W = RC * QP % 32 == 0 ? 32 : RC * QP % 16 == 0 ? 16 : 8;  // columns a load
-#pragma unroll
-                for (int c0 = 0; c0 < RC * QP; c0 += W) {
-                    float v[W];
-                    tmem_ld<W>(lanes + buf * N1 + c0, v);
-#pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        const int k = (c0 + i) / RC, r = (c0 + i) % RC;
-                        y[r] = k == 0 ? v[i] : fmaf(v[i], 1.f / (float)(1ull << (5 * k)), y[r]);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ms.s_free[buf]));
                 const int tile = u.tile(j), tok = tile * kTile + tid;
                 const uint32_t have = ms.ok[st];
                 const bool whole = have == all_slots && tile * kTile + kTile - 1 <= u.p0 &&
                                    (!a.window || tile * kTile > u.p1 - a.window || tile * kTile + kTile <= a.sinks);
                 const float ks = ms.ks[st][slot], vs = ms.vs[st][slot];
-                uint32_t vis = kFull;
+                uint32_t vis = real;
                 if (!whole) {
                     vis = 0;
                     if ((have >> slot) & 1u) {
@@ -372,21 +381,29 @@ __global__ void __launch_bounds__(kThreads, 2)
                         vis &= real;
                     }
                 }
-                float most = -INFINITY;
+                float z[RC];  // exponents of the weights: score - maximum + bias, log2 units
+                row_scores<RC, QP>(lanes + buf * N1, ks, z);
 #pragma unroll
                 for (int r = 0; r < RC; ++r) {
-                    y[r] *= ks;
-                    const float z = fmaf(y[r], ms.c[r], -ms.m[r]);
-                    if (r < u.rows && ((vis >> r) & 1u)) most = fmaxf(most, z);
+                    const float2 cb = ms.cb[r];
+                    z[r] = fmaf(z[r], cb.x, cb.y);
                 }
-                if (any_token(most > kLag || (vis != 0 && vs > vref))) {
+                if (vis != kFull) {
+#pragma unroll
+                    for (int r = 0; r < RC; ++r) z[r] = (vis >> r) & 1u ? z[r] : -INFINITY;
+                }
+                float most = z[0];
+#pragma unroll
+                for (int r = 1; r < RC; ++r) most = fmaxf(most, z[r]);
+                if (any_token(most > kBias + kLag || (vis != 0 && vs > vref))) {
                     // raise the maxima: per row over the tile's tokens, and the v scale
+                    row_scores<RC, QP>(lanes + buf * N1, ks, z);
 #pragma unroll
                     for (int r = 0; r < RC; ++r) {
-                        const float z = warp_max((vis >> r) & 1u ? y[r] * ms.c[r] : -INFINITY);
-                        if (lane == 0) ms.red[warp][r] = z;
+                        const float top = warp_max_f32((vis >> r) & 1u ? z[r] * ms.cb[r].x : -INFINITY);
+                        if (lane == 0) ms.red[warp][r] = top;
                     }
-                    const float top_v = warp_max(vis ? vs : 0.f);
+                    const float top_v = warp_max_f32(vis ? vs : 0.f);
                     if (lane == 0) ms.red[warp][32] = top_v;
                     bar_tokens();
                     const float vn = fmaxf(fmaxf(vref, fmaxf(ms.red[0][32], ms.red[1][32])),
@@ -396,11 +413,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float f[RC];
 #pragma unroll
                     for (int r = 0; r < RC; ++r) {
-                        const float m = ms.m[r];
-                        const float mn = fmaxf(fmaxf(m, fmaxf(ms.red[0][r], ms.red[1][r])),
+                        const float2 cb = ms.cb[r];
+                        const float mn = fmaxf(fmaxf(ms.m[r], fmaxf(ms.red[0][r], ms.red[1][r])),
                                                fmaxf(ms.red[2][r], ms.red[3][r]));
-                        f[r] = m == mn ? 1.f : exp2_approx(m - mn);
+                        f[r] = ms.m[r] == mn ? 1.f : exp2_approx(ms.m[r] - mn);
                         l[r] *= f[r];
+                        z[r] = (vis >> r) & 1u ? fmaf(z[r], cb.x, kBias - mn) : -INFINITY;
                     }
                     if (j > j0) {
                         wait(smem_u32(&ms.p_free[buf ^ 1]), ((it - 1) >> 1) & 1);
@@ -416,11 +434,17 @@ __global__ void __launch_bounds__(kThreads, 2)
                         tmem_wait_st();
                     }
                     bar_tokens();
-                    if (tid < RC)
-                        ms.m[tid] = fmaxf(fmaxf(ms.m[tid], fmaxf(ms.red[0][tid], ms.red[1][tid])),
-                                          fmaxf(ms.red[2][tid], ms.red[3][tid]));
+                    if (tid < RC) {
+                        const float mn = fmaxf(fmaxf(ms.m[tid], fmaxf(ms.red[0][tid], ms.red[1][tid])),
+                                               fmaxf(ms.red[2][tid], ms.red[3][tid]));
+                        ms.m[tid] = mn;
+                        ms.cb[tid].y = kBias - mn;
+                    }
                     bar_tokens();
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ms.s_free[buf]));
                 const float wv = vis && vref > 0.f ? vs / vref : 0.f;
                 uint32_t word[N2 / 4];
 #pragma unroll
@@ -430,8 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float w[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float p = exp2_approx(fmaf(y[r + i], ms.c[r + i], kBias - ms.m[r + i]));
-                        w[i] = (vis >> (r + i)) & 1u ? p : 0.f;
+                        w[i] = exp2_approx(z[r + i]);
                         l[r + i] += w[i];
                         w[i] *= wv;
                     }
@@ -500,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int k = (c0 + i) / RC, r = (c0 + i) % RC;
-                    if (k < PP) o[r] = k == 0 ? v[i] : fmaf(v[i], 1.f / (float)(1ull << (5 * k)), o[r]);
+                    if (k < PP) o[r] = k == 0 ? v[i] : fmaf(v[i], 1.f / (float)(1ull << (kShift * k)), o[r]);
                 }
             }
             tc_fence_before();
