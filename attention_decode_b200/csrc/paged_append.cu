@@ -375,6 +375,136 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
     }
 }
 
+// The same for calls of a row or two per sequence (a decode step): one warp per
+// (page slot, head), four rows at a time, in fp64 throughout, nothing shared.
+template <typename XT>
+__global__ void __launch_bounds__(128) paged_append_few_kernel(const __grid_constant__ PagedAppendArgs a) {
+    __shared__ double2 turned[4][4][64];  // (cos, sin) of a warp's four rows
+    const int lane = lane_id(), l = lane & 7, rg = lane >> 3;
+    const int heads = 2 * a.Hkv + (a.q ? a.Hq : 0);
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int64_t item = w / heads;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && a.seqs.status)
+        for (int b = threadIdx.x; b < a.seqs.B; b += 128) paged_report(a.seqs, paged_seq(a.seqs, b).bad);
+    if (item >= a.items) return;
+    int b = 0, slot = 0;
+    PagedSeq seq{};
+    if (!find_item(a.seqs, a.page, item, b, slot, seq)) return;
+    const int hh = (int)(w % heads), kind = hh < a.Hkv ? 0 : hh < 2 * a.Hkv ? 1 : 2;  // K, V, Q
+    const int h = hh - kind * a.Hkv, start = seq.len - seq.rows, t0 = slot * a.page;
+    const int first = start > t0 ? start - t0 : 0, last = seq.len - t0 < a.page ? seq.len - t0 : a.page;
+    const int64_t st = kind == 0 ? a.k_st : kind == 1 ? a.v_st : a.q_st;
+    const int64_t sh = kind == 0 ? a.k_sh : kind == 1 ? a.v_sh : a.q_sh;
+    const int64_t row0 = seq.row0 + t0 - start;
+    const XT* x = reinterpret_cast<const XT*>(kind == 0 ? a.k : kind == 1 ? a.v : a.q) + h * sh + row0 * st;
+    const bool rope = a.rope && kind != 1;
+    // Channels [8l, 8l + 8) of both halves of this lane's row of rows r0 .. r0 + 3,
+    // rotated. The whole warp computes a row's 64 angles, two a lane.
+    double lo[8], hi[8];
+    auto rotated = [&](int r0) {
+        const int r = r0 + rg;
+        float u[8], v[8];
+        if (r < last) {
+            load8f(x + r * st + 8 * l, u);
+            load8f(x + r * st + kD / 2 + 8 * l, v);
+        }
+        if (rope) {
+            double2(*cs)[64] = turned[threadIdx.x >> 5];
+            __syncwarp();
+#pragma unroll 1
+            for (int k = 0; k < 4 && r0 + k < last; ++k)
+#pragma unroll
+                for (int i = lane; i < 64; i += 32) sincospi(2.0 * (t0 + r0 + k) * a.turns[i], &cs[k][i].y, &cs[k][i].x);
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = hi[i] = 0.0;
+            if (r >= last) continue;
+            lo[i] = u[i];
+            hi[i] = v[i];
+            if (!rope) continue;
+            const double2 w = turned[threadIdx.x >> 5][rg][8 * l + i];
+            lo[i] = (double)u[i] * w.x - (double)v[i] * w.y;
+            hi[i] = (double)u[i] * w.y + (double)v[i] * w.x;
+        }
+    };
+    if (kind == 2) {
+#pragma unroll 1
+        for (int r0 = first; r0 < last; r0 += 4) {
+            const int r = r0 + rg;
+            rotated(r0);
+            if (r >= last) continue;
+            XT* o = reinterpret_cast<XT*>(a.q_out) + ((row0 + r) * a.Hq + h) * kD + 8 * l;
+            float u[8], v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = (float)lo[i], v[i] = (float)hi[i];
+            store8(o, u);
+            store8(o + kD / 2, v);
+        }
+        return;
+    }
+    const int64_t id = a.seqs.table[b * a.seqs.table_stride + slot];
+    if (id < 0 || id >= a.num_pages) {
+        if (lane == 0) paged_report(a.seqs, kBadPage);
+        return;
+    }
+    float* scale = (kind ? a.vs : a.ks) + id * a.Hkv + h;
+    uint8_t* codes = (kind ? a.vc : a.kc) + (id * a.Hkv + h) * (int64_t)(a.page * kD) + 8 * l;
+    const float old = first > 0 ? *scale : 0.f;
+    const bool had = old > 0.f && old < INFINITY;
+    double top = 0.0;
+#pragma unroll 1
+    for (int r0 = first; r0 < last; r0 += 4) {
+        rotated(r0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (isfinite(lo[i])) top = fmax(top, fabs(lo[i]));
+            if (isfinite(hi[i])) top = fmax(top, fabs(hi[i]));
+        }
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, m));
+    const bool keep = had && top <= 448.0 * (double)old;
+    const double s_new = keep ? (double)old : exp2i(cover_exponent(top)), inv = 1.0 / s_new;
+    __syncwarp();  // every lane has the old scale
+    if (lane == 0) *scale = (float)s_new;
+    if (!keep && had) {
+        const double ratio = (double)old / s_new;
+#pragma unroll 1
+        for (int r = rg; r < first; r += 4) {
+            renew_row(codes + r * kD, ratio);
+            renew_row(codes + r * kD + kD / 2, ratio);
+        }
+    }
+#pragma unroll 1
+    for (int r0 = first; r0 < last; r0 += 4) {
+        const int r = r0 + rg;
+        if (last - first > 4) rotated(r0);  // else the lane still holds its one row
+        if (r >= last) continue;
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            c[i] = e4m3x2(to_odd(lo[4 * i] * inv), to_odd(lo[4 * i + 1] * inv)) |
+                   (e4m3x2(to_odd(lo[4 * i + 2] * inv), to_odd(lo[4 * i + 3] * inv)) << 16);
+            c[2 + i] = e4m3x2(to_odd(hi[4 * i] * inv), to_odd(hi[4 * i + 1] * inv)) |
+                       (e4m3x2(to_odd(hi[4 * i + 2] * inv), to_odd(hi[4 * i + 3] * inv)) << 16);
+        }
+        *reinterpret_cast<uint2*>(codes + r * kD) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2*>(codes + r * kD + kD / 2) = make_uint2(c[2], c[3]);
+    }
+}
+
+template <typename XT>
+cudaError_t launch_few(const PagedAppendArgs& a, cudaStream_t s) {
+    static std::atomic<unsigned long long> ready{0};
+    const int64_t warps = a.items * (2 * a.Hkv + (a.q ? a.Hq : 0)), grid = (warps + 3) / 4;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    return launch_smem_pdl(paged_append_few_kernel<XT>, ready, dim3((unsigned)grid), dim3(128), 0, s, a);
+}
+
 template <typename XT, int PAGE>
 cudaError_t launch_page(const PagedAppendArgs& a, int64_t grid, cudaStream_t s) {
     static std::atomic<unsigned long long> ready{0};
@@ -394,6 +524,9 @@ cudaError_t launch_type(const PagedAppendArgs& a, int64_t grid, cudaStream_t s) 
 }  // namespace
 
 cudaError_t launch_paged_append(PagedAppendArgs a, bool bf16, cudaStream_t s) {
+    // A row or two per sequence: a page block would hold 64 threads and more to
+    // each row it has.
+    if (a.seqs.n_rows <= 2 * (int64_t)a.seqs.B) return bf16 ? launch_few<__nv_bfloat16>(a, s) : launch_few<float>(a, s);
     // Heads per block: more of them share a page's cos and sin (computing those
     // costs a block as much as two or three heads), as long as there are blocks
     // for every SM eight times over.

@@ -57,11 +57,16 @@ constexpr int kJoinThreads = 128;
 constexpr int kMaxParts = 640;  // CTAs of the largest grid (two per SM of up to 320) and one more
 
 // Block (c, y), c < grid: where a unit crosses into CTA c and began in c - 1,
-// each warp joins one of its rows, lane = 4 channels. Block (grid + b, y):
-// zeros for the rows of sequence b that lie in front of its first token.
+// joins rows of it, lane = 4 channels. A unit of few rows may be in many parts
+// (a long context over every CTA): the four warps then share a row's parts, in
+// a fixed order. A unit of many rows is in two or three: a warp takes a row.
+// Block (grid + b, y): zeros for the rows of sequence b in front of its first
+// token.
 template <int RC>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
-    __shared__ float factor[kJoinThreads / 32][kMaxParts];
+    constexpr int kWarps = kJoinThreads / 32, kShare = RC <= 32 ? kWarps : 1;  // warps to a row
+    __shared__ float factor[kWarps][kMaxParts / kShare + 1];
+    __shared__ float4 sums[kWarps][32];
     const int lane = lane_id(), warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((int)blockIdx.x >= grid) {
@@ -74,12 +79,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         return;
     }
     const PagedSeam seam = a.seams[blockIdx.x];
-    const int r = blockIdx.y * (kJoinThreads / 32) + warp;
-    if (!seam.live || r >= seam.rows) return;
-    const int c = blockIdx.x, n = seam.last - c + 2;
+    const int r = blockIdx.y * (kWarps / kShare) + warp / kShare;
+    if (!seam.live || r >= seam.rows) return;  // (with shared rows, the whole block)
+    const int c = blockIdx.x, n = seam.last - c + 2, w0 = warp % kShare;
     auto part = [&](int k) { return a.part + (k ? 2 * (c + k - 1) : seam.first) * part_stride<RC>(); };
     float top = -INFINITY;
-#pragma unroll 1
     for (int k = lane; k < n; k += 32) {
         const float* p = part(k) + RC * kD + r;
         const float m = p[0], l = p[RC];
@@ -87,25 +91,34 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     }
     top = warp_max(top);
     float sum = 0.f;
-#pragma unroll 1
     for (int k = lane; k < n; k += 32) {
         const float* p = part(k) + RC * kD + r;
         const float m = p[0], l = p[RC];
         const float f = l != 0.f ? exp2_approx(m - top) : 0.f;
-        factor[warp][k] = f;
+        if (k % kShare == w0) factor[warp][k / kShare] = f;
         if (l != 0.f) sum = fmaf(f, l, sum);
     }
     sum = warp_sum(sum);
     __syncwarp();
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) {
+    for (int k = w0; k < n; k += kShare) {
         const float4 v = *reinterpret_cast<const float4*>(part(k) + r * kD + 4 * lane);
-        const float f = factor[warp][k];
+        const float f = factor[warp][k / kShare];
         const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (f != 0.f) acc[i] = fmaf(f, w[i], acc[i]);
+    }
+    if (kShare > 1) {
+        sums[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        __syncthreads();
+        if (warp) return;
+#pragma unroll
+        for (int w = 1; w < kShare; ++w) {
+            const float4 v = sums[w][lane];
+            acc[0] += v.x; acc[1] += v.y; acc[2] += v.z; acc[3] += v.w;
+        }
     }
     const int rr = seam.r0 + r, i = (int)fdiv((uint32_t)rr, a.G), G = (int)a.G.d;
     const int64_t at = ((int64_t)(seam.row0 + i) * a.Hq + seam.h * G + rr - i * G) * kD + 4 * lane;
@@ -122,7 +135,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 template <int RC>
 cudaError_t launch_paged_join(const PagedAttnArgs& a, int grid, cudaStream_t s) {
     static std::atomic<unsigned long long> ready{0};
-    return launch_smem_pdl(paged_join_kernel<RC>, ready, dim3(grid + a.seqs.B, RC / 4), dim3(kJoinThreads), 0, s, a,
+    return launch_smem_pdl(paged_join_kernel<RC>, ready, dim3(grid + a.seqs.B, RC <= 32 ? RC : RC / 4), dim3(kJoinThreads), 0, s, a,
                            grid);
 }
 
