@@ -32,20 +32,21 @@ nsnq_status check_paged(const nsnq_paged_cache& c, const int32_t* cu_rows, const
         return set_error(NSNQ_ERR_UNSUPPORTED, "cache.page_size = %d (16, 32, 64 or 128 supported)", c.page_size);
     if (c.heads != Hkv)
         return set_error(NSNQ_ERR_INVALID_ARG, "cache.heads = %d differs from Hkv = %d", c.heads, Hkv);
-    if (c.num_pages < 0) return set_error(NSNQ_ERR_INVALID_ARG, "cache.num_pages = %lld < 0", (long long)c.num_pages);
+    if (c.num_pages <= 0)
+        return set_error(NSNQ_ERR_INVALID_ARG, "cache.num_pages = %lld (at least 1)", (long long)c.num_pages);
     if (c.num_pages >= ((int64_t)1 << 31) / Hkv)
         return set_error(NSNQ_ERR_UNSUPPORTED, "cache.num_pages * heads = %lld * %d (limit 2^31)",
                          (long long)c.num_pages, Hkv);
     if (table_cols < 0 || table_stride < table_cols)
         return set_error(NSNQ_ERR_INVALID_ARG, "need 0 <= table_cols <= table_stride (%lld, %lld)",
                          (long long)table_cols, (long long)table_stride);
-    if (c.num_pages > 0 && (!c.k || !c.v || !c.k_scales || !c.v_scales))
+    if (!c.k || !c.v || !c.k_scales || !c.v_scales)
         return set_error(NSNQ_ERR_INVALID_ARG, "cache has a NULL buffer");
     if (!aligned(c.k, 128) || !aligned(c.v, 128))
         return set_error(NSNQ_ERR_INVALID_ARG, "cache.k and cache.v must be 128-byte aligned");
     if (!aligned(c.k_scales, 4) || !aligned(c.v_scales, 4) || !aligned(c.status, 4))
         return set_error(NSNQ_ERR_INVALID_ARG, "cache scales and status must be 4-byte aligned");
-    if (c.k && (c.k == c.v || c.k_scales == c.v_scales))
+    if (c.k == c.v || c.k_scales == c.v_scales)
         return set_error(NSNQ_ERR_INVALID_ARG, "keys and values of the cache share a buffer");
     if (B > 0 && n_rows > 0) {
         if (!seq_lens || (table_cols > 0 && !table))

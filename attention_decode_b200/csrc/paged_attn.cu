@@ -36,7 +36,7 @@ constexpr int kThreads = 192;  // warps 0-3: tokens / channels; 4: TMA; 5: MMA i
 constexpr float kLag = 5.f, kBias = 2.f;  // weights stay below 2^7 (1 + 2^-20)
 constexpr int kShift = 6;                  // bits between the pieces of a weight
 constexpr int kMaxSlots = 8;   // pages per tile (page_size 16)
-constexpr int kSetup = 1;      // tiles that a unit's queries and epilogue cost
+constexpr int kSetup = 3;      // tiles that a unit's queries and epilogue cost
 
 constexpr int pad16(int n) { return (n + 15) / 16 * 16; }
 constexpr int pow2_at_least(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }

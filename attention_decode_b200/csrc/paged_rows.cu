@@ -31,7 +31,7 @@ constexpr int kThreads = 512;   // warps 0-3, 4-7: rows; 8-11: V to fp16; 12: TM
 constexpr float kLag = 12.f, kBias = 3.f;
 constexpr int kKStages = 3, kRing = 8;
 constexpr int kMaxSlots = 8;
-constexpr int kSetup = 3;       // tiles that a unit's queries and epilogue cost
+constexpr int kSetup = 5;       // tiles that a unit's queries and epilogue cost
 
 // shared memory, from a 1024-aligned base
 constexpr uint32_t kQ = 0;                        // [half][piece][128 rows][128 B]
@@ -145,16 +145,17 @@ struct RowState {
     float vref, rv;    // largest v scale so far and its reciprocal
 };
 
-// Multiplies a row's weights of the step so far (`done` columns of fp16 pairs,
-// 0 or 16) and, if there is one, its output by a factor.
+// Multiplies a row's weights of the step so far (`done` columns of fp16 pairs) and,
+// if there is one, its output by a factor.
 __device__ __noinline__ void rescale_row(uint32_t s, int done, uint32_t o, bool have_o, float f) {
-    if (done) {
-        const uint32_t f2 = f16x2(f, f);
-        uint32_t u[16];
-        TmemLoad<16>::run(s, u);
+    const uint32_t f2 = f16x2(f, f);
+#pragma unroll 1
+    for (int i = 0; i < done; i += 8) {
+        uint32_t u[8];
+        TmemLoad<8>::run(s + i, u);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) asm("mul.f16x2 %0, %1, %2;" : "=r"(u[k]) : "r"(u[k]), "r"(f2));
-        tmem_st16(s, u);
+        for (int k = 0; k < 8; ++k) asm("mul.f16x2 %0, %1, %2;" : "=r"(u[k]) : "r"(u[k]), "r"(f2));
+        tmem_st8(s + i, reinterpret_cast<float*>(u));
     }
 #pragma unroll 1
     for (int i = 0; have_o && i < kD; i += 16) {
@@ -167,104 +168,95 @@ __device__ __noinline__ void rescale_row(uint32_t s, int done, uint32_t o, bool 
     tmem_wait_st();
 }
 
-// Weights of 32 columns of a row from their scores u: exponents, the largest
-// of them, 2^x, their sum; packed in fp16 pairs.
-template <bool MASKED>
-__device__ __forceinline__ void row_weights(const uint32_t (&u)[32], uint32_t seen, const float2 (&kv)[2],
-                                            const RowState& st, float& most, float& sum, uint32_t (&p)[16]) {
+// Weights of 16 columns of a row from their scores u: exponents, the largest
+// of them, 2^x, their sum; packed in fp16 pairs. WEIGH: some page's v scale is
+// not the largest so far. (Exponents are formed in packed pairs, as the scores
+// lie; what follows 2^x is scalar: packing it again costs more moves than it saves.)
+template <bool MASKED, bool WEIGH>
+__device__ __forceinline__ void row_weights(const uint32_t (&u)[16], uint32_t seen, float2 kv, const RowState& st,
+                                            float& most, float& sum, uint32_t (&p)[8]) {
     const uint64_t nm = pk2(kBias - st.m, kBias - st.m);
-    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+    const float f = kv.x * st.c, w = kv.y * st.rv;
+    const uint64_t f2 = pk2(f, f);
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const float f = kv[g].x * st.c, w = kv[g].y * st.rv;
-        const uint64_t f2 = pk2(f, f), w2 = pk2(w, w);
-        const bool weigh = w != 1.f;
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const int at = 16 * g + i;
-            float2 x = upk2(fma2(pk2(__uint_as_float(u[at]), __uint_as_float(u[at + 1])), f2, nm));
-            if (MASKED) {
-                x.x = (seen >> at) & 1u ? x.x : -INFINITY;
-                x.y = (seen >> at) & 2u ? x.y : -INFINITY;
-            }
-            top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(x.x, x.y));
-            v[i] = exp2_approx(x.x);
-            v[i + 1] = exp2_approx(x.y);
-            acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pk2(v[i], v[i + 1]));
+    for (int i = 0; i < 16; i += 2) {
+        float2 x = upk2(fma2(pk2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), f2, nm));
+        if (MASKED) {
+            x.x = (seen >> i) & 1u ? x.x : -INFINITY;
+            x.y = (seen >> i) & 2u ? x.y : -INFINITY;
         }
-        if (weigh) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                float2 y = upk2(mul2(pk2(v[i], v[i + 1]), w2));
-                if (MASKED) {  // the scale of a page that was not loaded is void
-                    y.x = (seen >> (16 * g + i)) & 1u ? y.x : 0.f;
-                    y.y = (seen >> (16 * g + i)) & 2u ? y.y : 0.f;
-                }
-                v[i] = y.x;
-                v[i + 1] = y.y;
+        top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(x.x, x.y));
+        x.x = exp2_approx(x.x);
+        x.y = exp2_approx(x.y);
+        acc[(i >> 1) & 1] += x.x;
+        acc[2 + ((i >> 1) & 1)] += x.y;
+        if (WEIGH) {
+            x.x *= w;
+            x.y *= w;
+            if (MASKED) {  // the scale of a page that was not loaded is void
+                x.x = (seen >> i) & 1u ? x.x : 0.f;
+                x.y = (seen >> i) & 2u ? x.y : 0.f;
             }
         }
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) p[8 * g + i / 2] = f16x2(v[i], v[i + 1]);
+        p[i / 2] = f16x2(x.x, x.y);
     }
     most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    const float2 t = upk2(add2(acc[0], acc[1]));
-    sum = t.x + t.y;
+    sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
-// Raises a row's maximum to that of columns 32 q .. 32 q + 31 (their scores are
-// still in TMEM) and scales the weights and outputs so far; returns the new
-// maximum and the factor.
-__device__ __noinline__ float2 raise_row(uint32_t s, uint32_t o, bool have_o, int q, uint32_t seen, float f0, float f1,
-                                         bool real, float m) {
+// Raises a row's maximum to that of columns 16 q .. 16 q + 15 of the step (their
+// scores are still in TMEM) and scales the weights and outputs so far; returns
+// the new maximum and the factor.
+__device__ __noinline__ float2 raise_row(uint32_t s, uint32_t o, bool have_o, int q, uint32_t seen, float f0, bool real,
+                                         float m) {
     float top = -INFINITY;
 #pragma unroll 1
-    for (int i = 0; i < 32; i += 8) {
+    for (int i = 0; i < 16; i += 8) {
         float v[8];
-        tmem_ld<8>(s + 32 * q + i, v);
-        const float f = i < 16 ? f0 : f1;
+        tmem_ld<8>(s + 16 * q + i, v);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if ((seen >> (i + k)) & 1u) top = fmaxf(top, v[k] * f);
+            if ((seen >> (i + k)) & 1u) top = fmaxf(top, v[k] * f0);
     }
     const float mn = real ? fmaxf(m, top) : 0.f;
     const float f = m == mn ? 1.f : exp2_approx(m - mn);
-    rescale_row(s, 16 * q, o, have_o, f);
+    rescale_row(s, 8 * q, o, have_o, f);
     return make_float2(mn, f);
 }
 
-// The weights of a row over step b of a tile (64 tokens), 32 columns at a time,
-// over the front of its scores: column pair i of P takes the place of score
-// i, which has been read by then. Where a chunk's largest exponent passes the
-// lag, the warp raises its rows' maxima first.
-template <bool MASKED>
+// The weights of a row over step b of a tile (64 tokens), 16 columns at a time,
+// over the front of its scores: column pair i of P takes the place of score i,
+// which has been read by then. Where a chunk's largest exponent passes the lag,
+// the warp raises its rows' maxima first. (Short loops: 32 columns at a time
+// took 2 % longer, 64 in a row 15 %: eight warps run this code each at a place
+// of its own, and fetching longer code costs more than its overlap gains.)
+template <bool MASKED, bool WEIGH>
 __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, int b, const float2* scale, int page_log,
                                          bool real, const View& view, RowState& st, Waiter& wait, uint32_t pv_done) {
 #pragma unroll 1
-    for (int q = 0; q < 2; ++q) {
-        const int col = 64 * b + 32 * q;
-        const uint32_t seen = MASKED ? view.bits(col) : kFull;
-        const float2 kv[2] = {scale[col >> page_log], scale[(col + 16) >> page_log]};
-        uint32_t u[32];
-        TmemLoad<32>::run(s + 32 * q, u);
+    for (int q = 0; q < 4; ++q) {
+        const int col = 64 * b + 16 * q;
+        const uint32_t seen = MASKED ? view.bits(col & ~31) >> (col & 31) : kFull;
+        const float2 kv = scale[col >> page_log];
+        uint32_t u[16];
+        TmemLoad<16>::run(s + 16 * q, u);
         float most, sum;
-        uint32_t p[16];
-        row_weights<MASKED>(u, seen, kv, st, most, sum, p);
+        uint32_t p[8];
+        row_weights<MASKED, WEIGH>(u, seen, kv, st, most, sum, p);
         if (__any_sync(kFull, real && most > kBias + kLag)) {
             if (have_o) {  // O is quiet once the step before is done
                 wait(pv_done, b ^ 1);
                 tc_fence_after();
             }
-            const float2 r = raise_row(s, o, have_o, q, seen, kv[0].x * st.c, kv[1].x * st.c, real, st.m);
+            const float2 r = raise_row(s, o, have_o, q, seen, kv.x * st.c, real, st.m);
             st.m = r.x;
             st.l *= r.y;
-            TmemLoad<32>::run(s + 32 * q, u);
-            row_weights<MASKED>(u, seen, kv, st, most, sum, p);
+            TmemLoad<16>::run(s + 16 * q, u);
+            row_weights<MASKED, WEIGH>(u, seen, kv, st, most, sum, p);
         }
         st.l += sum;
-        tmem_st16(s + 16 * q, p);
+        tmem_st8(s + 8 * q, reinterpret_cast<float*>(p));
     }
     tmem_wait_st();
 }
@@ -524,6 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int j = j0; j < j1; ++j, ++it, ++n) {
                     const uint32_t ring = it % kRing;
+                    // The scores first: a half without rows skips whole segments, and only
+                    // with them is the ring's phase known to be this tile's or the one before.
+                    wait(smem_u32(&ms.s_full[hf][0]), n & 1);
                     wait(smem_u32(&ms.sc_full[ring]), (it / kRing) & 1);
                     const int t0 = u.tile(j) * kTile;
                     const uint32_t ok = ms.ok[ring];
@@ -534,6 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (scales are positive: their bits order like them)
                     const float vmax = __uint_as_float(__reduce_max_sync(
                         kFull, lane < slots && ((ok >> lane) & 1u) ? __float_as_uint(scale[lane].y) : 0u));
+                    const float vmin = __uint_as_float(__reduce_min_sync(
+                        kFull, lane < slots && ((ok >> lane) & 1u) ? __float_as_uint(scale[lane].y) : 0x7f800000u));
+                    const bool plain = whole && vmin >= fmaxf(vmax, st.vref);
 #pragma unroll 1
                     for (int b = 0; b < 2; ++b) {
                         wait(smem_u32(&ms.s_full[hf][b]), n & 1);
@@ -549,8 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             st.vref = vmax;
                             st.rv = 1.f / vmax;
                         }
-                        if (whole) row_step<false>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
-                        else row_step<true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
+                        if (plain) row_step<false, false>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
+                        else if (whole) row_step<false, true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
+                        else row_step<true, true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&ms.p_full[hf][b]));

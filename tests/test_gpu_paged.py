@@ -252,6 +252,53 @@ def test_attention(new, before, hq, hkv, page, window, sinks, dtype):
     pc.check()
 
 
+def dense64(q, b, pc, table, window, sinks, scale):
+    """fp64 attention on the device, a sequence and kv-head at a time: out, weight, reach, spread as the oracle's."""
+    n, hq = b.cu[-1], b.hq
+    out, weight = (torch.zeros(n, hq, D, dtype=torch.float64, device="cuda") for _ in range(2))
+    reach, spread = (torch.zeros(n, hq, 1, dtype=torch.float64, device="cuda") for _ in range(2))
+    for s, length in enumerate(b.lens):
+        ids = table[s, :-(-length // b.page)].long()
+        rows, pos = slice(b.cu[s], b.cu[s + 1]), torch.arange(b.before[s], length, device="cuda")[:, None, None]
+        t = torch.arange(length, device="cuda")
+        seen = (t <= pos) & ((t > pos - window) | (t < sinks) if window else True)
+        for h in range(b.hkv):
+            k, v = ((c.view(torch.uint8)[ids, h].view(torch.float8_e4m3fn).double() * e[ids, h].double()[:, None, None])
+                    .reshape(-1, D)[:length] for c, e in ((pc.k, pc.k_scales), (pc.v, pc.v_scales)))
+            g = slice(h * (hq // b.hkv), (h + 1) * (hq // b.hkv))
+            qq = q[rows, g].double()
+            p = torch.softmax((qq @ k.T * scale).masked_fill(~seen, -math.inf), -1)
+            out[rows, g], weight[rows, g] = p @ v, p @ v.abs()
+            reach[rows, g] = (qq.abs() @ k.abs().T * scale).masked_fill(~seen, 0).amax(-1, keepdim=True)
+            spread[rows, g] = seen.sum(-1, keepdim=True) * v.abs().max()
+    return out, weight, reach, spread
+
+
+@pytest.mark.parametrize("new,before,hq,hkv,page,window,sinks", [
+    # enough tiles that a CTA takes several units, with last units of one row, of half a unit and less
+    ([280, 65, 129, 320], [1500, 3000, 700, 0], 32, 8, 16, 0, 0),
+    ([280, 280, 33, 97], [2500, 1111, 4000, 3000], 8, 8, 128, 0, 0),
+    ([350, 77, 513], [3000, 2000, 900], 20, 4, 64, 600, 9),
+    ([2048], [0], 16, 4, 32, 0, 0),
+    ([1] * 70, [(97 * i) % 3000 for i in range(70)], 24, 8, 64, 0, 0),
+    ([4, 1, 3] * 12, [(531 * i) % 5000 for i in range(36)], 16, 4, 16, 1000, 130),
+    ([8, 5] * 9, [(731 * i) % 4000 for i in range(18)], 32, 8, 32, 0, 0),
+    ([2] * 5, [30000, 7, 12000, 20001, 1], 32, 8, 128, 0, 0),
+])
+def test_attention_many_units(new, before, hq, hkv, page, window, sinks):
+    b = Batch(new, before, hq, hkv, page, seed=sum(new) + page)
+    b.tails(0x7F)
+    pc, (table, lens, cu), q = b.cache(), b.dev(), b.q.cuda()
+    want, weight, reach, spread = dense64(q, b, pc, table, window, sinks, 1 / math.sqrt(D))
+    e = 2.0 ** -18 + 160 * 2.0 ** -23 * reach + 2.0 ** -11
+    tol = 2.0 ** -8 * want.abs() + 2 * e * weight + 2.0 ** -24 * spread
+    for _ in range(3):
+        got = nsnq.nsnq_paged_attn(q, pc, table, lens, cu, max_rows=max(new), window=window, sinks=sinks).double()
+        err = (got - want).abs()
+        assert (err <= tol).all(), (torch.nonzero(~(err <= tol))[:5], (err / tol).max())
+    pc.check()
+
+
 @pytest.mark.parametrize("rows", [1, 5, 140])
 def test_attention_types_mixed_scale_given(rows):
     b = Batch([rows, rows], [90, 300], 4, 2, 16, seed=rows)

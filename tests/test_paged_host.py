@@ -58,6 +58,7 @@ BOTH = [
     (dict(cache=dict(page=256)), nsnq.NSNQ_ERR_UNSUPPORTED, b"page_size"),
     (dict(cache=dict(heads=3)), nsnq.NSNQ_ERR_INVALID_ARG, b"heads"),
     (dict(cache=dict(pages=-1)), nsnq.NSNQ_ERR_INVALID_ARG, b"num_pages"),
+    (dict(cache=dict(pages=0)), nsnq.NSNQ_ERR_INVALID_ARG, b"num_pages"),
     (dict(cache=dict(pages=1 << 30)), nsnq.NSNQ_ERR_UNSUPPORTED, b"num_pages"),
     (dict(cache=dict(k=None)), nsnq.NSNQ_ERR_INVALID_ARG, b"NULL"),
     (dict(cache=dict(vs=None)), nsnq.NSNQ_ERR_INVALID_ARG, b"NULL"),
