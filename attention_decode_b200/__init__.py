@@ -644,39 +644,49 @@ class PagedCache:
         return c
 
 
-def _paged_seqs(dev, n_rows, page_table, seq_lens, cu_rows):
+# A decode step's calls take a few microseconds on the device, so these two
+# functions ask each tensor as little as they can: get_device() instead of
+# device, one stride() each, the current stream's handle without its object.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _paged_seqs(index, n_rows, page_table, seq_lens, cu_rows):
     """Checks of the device arrays that describe a call's sequences; returns
     (sequences, table columns, table row stride, cu_rows' address)."""
     i32 = torch.int32
     if page_table.dtype is not i32 or seq_lens.dtype is not i32 or (cu_rows is not None and cu_rows.dtype is not i32):
         raise TypeError("page_table, seq_lens and cu_rows must be int32")
-    if seq_lens.dim() != 1 or page_table.dim() != 2 or seq_lens.device != dev or page_table.device != dev:
-        raise ValueError(f"seq_lens must be [B] and page_table [B][columns], on {dev}")
-    B = seq_lens.shape[0]
+    if seq_lens.dim() != 1 or page_table.dim() != 2 or seq_lens.get_device() != index \
+            or page_table.get_device() != index:
+        raise ValueError(f"seq_lens must be [B] and page_table [B][columns], on device {index}")
+    B = len(seq_lens)
     rows, cols = page_table.shape
     stride, step = page_table.stride()
     if rows != B:
         raise ValueError(f"page_table has {rows} rows for {B} sequences")
-    if (cols > 1 and step != 1) or (B > 1 and seq_lens.stride(0) != 1):
+    if (cols > 1 and step != 1) or (B > 1 and not seq_lens.is_contiguous()):
         raise ValueError("seq_lens and the rows of page_table must be contiguous")
+    if stride < cols:
+        if rows > 1:
+            raise ValueError("the rows of page_table overlap")
+        stride = cols
     if cu_rows is None:
         if n_rows != B:
             raise ValueError(f"{n_rows} rows for {B} sequences: pass cu_rows")
-        return B, cols, max(stride, cols), None
-    if cu_rows.dim() != 1 or cu_rows.shape[0] != B + 1 or cu_rows.device != dev or (B and cu_rows.stride(0) != 1):
-        raise ValueError(f"cu_rows must hold {B + 1} contiguous entries on {dev}")
-    return B, cols, max(stride, cols), cu_rows.data_ptr()
+        return B, cols, stride, None
+    if cu_rows.shape != (B + 1,) or cu_rows.get_device() != index or not cu_rows.is_contiguous():
+        raise ValueError(f"cu_rows must hold {B + 1} contiguous entries on device {index}")
+    return B, cols, stride, cu_rows.data_ptr()
 
 
-def _on_stream(dev, stream, call):
-    """call(raw stream) with the device of its tensors current and, with it, the
-    given stream, so that what the call allocates belongs to the stream that
-    uses it."""
+def _paged_on(index, stream, call):
+    """call(raw stream) with device `index` current and, with it, the given
+    stream, so that what the call allocates belongs to the stream that uses it."""
+    dev = torch.device("cuda", index)
     if stream is None:
-        if dev.index == torch.cuda.current_device():
-            return call(torch.cuda.current_stream().cuda_stream)
         with torch.cuda.device(dev):
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(_current_raw_stream(index))
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     if stream.device != dev:
@@ -695,34 +705,38 @@ def nsnq_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, page_
     tokens: seq_lens[b] counts its tokens with them. page_table [B][columns]
     lists each sequence's pages. With q [rows][Hq][D], returns q rotated the
     same way (into q_out if given)."""
-    c, dev, dtype = cache._c(), k.device, k.dtype
-    N, H, D = shape = k.shape
-    ks, vs = k.stride(), v.stride()
-    if v.shape != shape or v.dtype is not dtype or ks[2] != 1 or vs[2] != 1:
+    c, index, dtype = cache._c(), k.get_device(), k.dtype
+    N, H, D = k.shape
+    k_t, k_h, k_d = k.stride()
+    v_t, v_h, v_d = v.stride()
+    if v.shape != k.shape or v.dtype is not dtype or k_d != 1 or v_d != 1:
         raise ValueError("k and v must have the same shape and dtype and contiguous channels")
-    if dev != cache.k.device or v.device != dev:
-        raise ValueError("k, v and the cache must be on one device")
-    B, cols, stride, cu = _paged_seqs(dev, N, page_table, seq_lens, cu_rows)
+    if index < 0 or cache.k.get_device() != index or v.get_device() != index:
+        raise ValueError("k, v and the cache must be on one CUDA device")
+    code = _dtype_code(k)
+    B, cols, row_stride, cu = _paged_seqs(index, N, page_table, seq_lens, cu_rows)
     if q is None:
-        q_out, Hq, qs, qp = None, H, (0, 0), None
+        q_out, Hq, q_t, q_h, q_at = None, H, 0, 0, None
     else:
-        qn, Hq, qd = q_shape = q.shape
-        qs, qp = q.stride(), q.data_ptr()
-        if qn != N or qd != D or q.dtype is not dtype or qs[2] != 1 or q.device != dev:
+        qn, Hq, qd = q.shape
+        q_t, q_h, q_d = q.stride()
+        q_at = q.data_ptr()
+        if qn != N or qd != D or q.dtype is not dtype or q_d != 1 or q.get_device() != index:
             raise ValueError("q must be [rows][Hq][D] like k, with contiguous channels")
-        if q_out is not None and (q_out.shape != q_shape or q_out.dtype is not dtype or q_out.device != dev
-                                  or not q_out.is_contiguous()):
+        if q_out is not None and (q_out.shape != q.shape or q_out.dtype is not dtype
+                                  or q_out.get_device() != index or not q_out.is_contiguous()):
             raise ValueError("q_out must be contiguous, of q's shape and dtype")
 
     def call(raw):
-        out = torch.empty(q_shape, dtype=dtype, device=dev) if q is not None and q_out is None else q_out
-        _check(load().nsnq_paged_append(k.data_ptr(), v.data_ptr(), qp, None if out is None else out.data_ptr(),
-                                        _dtype_code(k), N, ks[0], ks[1], vs[0], vs[1], qs[0], qs[1], cu,
-                                        seq_lens.data_ptr(), B, Hq, H, D, rope_base, c, page_table.data_ptr(),
-                                        cols, stride, raw))
+        out = q_out if q is None or q_out is not None else q.new_empty((N, Hq, D))
+        _check(load().nsnq_paged_append(k.data_ptr(), v.data_ptr(), q_at, None if out is None else out.data_ptr(),
+                                        code, N, k_t, k_h, v_t, v_h, q_t, q_h, cu, seq_lens.data_ptr(), B, Hq, H,
+                                        D, rope_base, c, page_table.data_ptr(), cols, row_stride, raw))
         return out
 
-    return _on_stream(dev, stream, call)
+    if stream is None and index == torch.cuda.current_device():
+        return call(_current_raw_stream(index))
+    return _paged_on(index, stream, call)
 
 
 def nsnq_paged_attn_workspace(n_rows: int, B: int, Hq: int, Hkv: int, max_rows: int, D: int = HEAD_DIM) -> int:
@@ -738,26 +752,28 @@ def nsnq_paged_attn(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     the last tokens of their sequences, over the paged cache: returns
     [rows][Hq][D]. max_rows bounds the rows of a sequence. With window > 0 a
     row sees the last `window` tokens up to its own and the first `sinks`."""
-    c, dev = cache._c(), q.device
-    N, Hq, D = shape = q.shape
-    qs = q.stride()
-    if qs[2] != 1 or dev != cache.k.device:
+    c, index = cache._c(), q.get_device()
+    N, Hq, D = q.shape
+    q_t, q_h, q_d = q.stride()
+    if q_d != 1 or index < 0 or cache.k.get_device() != index:
         raise ValueError("q must have contiguous channels and be on the cache's device")
-    B, cols, stride, cu = _paged_seqs(dev, N, page_table, seq_lens, cu_rows)
-    if out is not None and (out.shape != shape or out.device != dev or not out.is_contiguous()):
+    code = _dtype_code(q)
+    B, cols, row_stride, cu = _paged_seqs(index, N, page_table, seq_lens, cu_rows)
+    if out is not None and (out.shape != q.shape or out.get_device() != index or not out.is_contiguous()):
         raise ValueError("out must be contiguous, of q's shape")
-    if workspace is not None and workspace.device != dev:
+    if workspace is not None and workspace.get_device() != index:
         raise ValueError("the workspace must be on the cache's device")
 
     def call(raw):
-        to = torch.empty(shape, dtype=out_dtype, device=dev) if out is None else out
+        to = q.new_empty((N, Hq, D), dtype=out_dtype) if out is None else out
         ws = workspace
         if ws is None:
-            ws = _workspace(nsnq_paged_attn_workspace(N, B, Hq, c.heads, max_rows, D), dev)
-        _check(load().nsnq_paged_attn(q.data_ptr(), _dtype_code(q), N, qs[0], qs[1], cu, max_rows,
-                                      seq_lens.data_ptr(), B, Hq, c.heads, D, c, page_table.data_ptr(), cols,
-                                      stride, window, sinks, softmax_scale, to.data_ptr(), _dtype_code(to),
-                                      ws.data_ptr(), ws.nbytes, raw))
+            ws = _workspace(nsnq_paged_attn_workspace(N, B, Hq, c.heads, max_rows, D), to.device)
+        _check(load().nsnq_paged_attn(q.data_ptr(), code, N, q_t, q_h, cu, max_rows, seq_lens.data_ptr(), B, Hq,
+                                      c.heads, D, c, page_table.data_ptr(), cols, row_stride, window, sinks,
+                                      softmax_scale, to.data_ptr(), _dtype_code(to), ws.data_ptr(), ws.nbytes, raw))
         return to
 
-    return _on_stream(dev, stream, call)
+    if stream is None and index == torch.cuda.current_device():
+        return call(_current_raw_stream(index))
+    return _paged_on(index, stream, call)

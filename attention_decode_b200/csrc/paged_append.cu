@@ -174,7 +174,6 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
     const int64_t item = blockIdx.x / (2 * gkv + gq);
     int group = (int)(blockIdx.x % (2 * gkv + gq));
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && a.seqs.status)
         for (int b = threadIdx.x; b < a.seqs.B; b += kThreads) paged_report(a.seqs, paged_seq(a.seqs, b).bad);
     int b = 0, slot = 0;
@@ -363,7 +362,7 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
                 const float xa = (float)row[i], xb = (float)row[kD / 2 + i];
                 double2 v = make_double2(xa, xb);
                 if (rope) v = exact_pair(xa, xb, t0 + r, a.freq[i]);
-                const uint32_t c = e4m3x2(to_odd((k < 8 ? v.x : v.y) * inv_d), 0.f) & 0xffu;
+                const uint32_t c = e4m3x2(to_odd((k < 8 ? v.x : v.y) / s_new), 0.f) & 0xffu;
                 const int at = (k & 3) * 8;
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
@@ -385,7 +384,6 @@ __global__ void __launch_bounds__(128) paged_append_few_kernel(const __grid_cons
     const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int64_t item = w / heads;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && a.seqs.status)
         for (int b = threadIdx.x; b < a.seqs.B; b += 128) paged_report(a.seqs, paged_seq(a.seqs, b).bad);
     if (item >= a.items) return;
@@ -468,7 +466,12 @@ __global__ void __launch_bounds__(128) paged_append_few_kernel(const __grid_cons
 #pragma unroll
     for (int m = 16; m; m >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, m));
     const bool keep = had && top <= 448.0 * (double)old;
-    const double s_new = keep ? (double)old : exp2i(cover_exponent(top)), inv = 1.0 / s_new;
+    const double s_new = keep ? (double)old : exp2i(cover_exponent(top));
+    // a power of two is multiplied by its inverse; a caller's own scale divides
+    const double inv = (__float_as_uint((float)s_new) & 0x7fffffu) ? 0.0 : 1.0 / s_new;
+    auto code = [&](double a, double b) {
+        return inv != 0.0 ? e4m3x2(to_odd(a * inv), to_odd(b * inv)) : e4m3x2(to_odd(a / s_new), to_odd(b / s_new));
+    };
     __syncwarp();  // every lane has the old scale
     if (lane == 0) *scale = (float)s_new;
     if (!keep && had) {
@@ -487,10 +490,8 @@ __global__ void __launch_bounds__(128) paged_append_few_kernel(const __grid_cons
         uint32_t c[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            c[i] = e4m3x2(to_odd(lo[4 * i] * inv), to_odd(lo[4 * i + 1] * inv)) |
-                   (e4m3x2(to_odd(lo[4 * i + 2] * inv), to_odd(lo[4 * i + 3] * inv)) << 16);
-            c[2 + i] = e4m3x2(to_odd(hi[4 * i] * inv), to_odd(hi[4 * i + 1] * inv)) |
-                       (e4m3x2(to_odd(hi[4 * i + 2] * inv), to_odd(hi[4 * i + 3] * inv)) << 16);
+            c[i] = code(lo[4 * i], lo[4 * i + 1]) | (code(lo[4 * i + 2], lo[4 * i + 3]) << 16);
+            c[2 + i] = code(hi[4 * i], hi[4 * i + 1]) | (code(hi[4 * i + 2], hi[4 * i + 3]) << 16);
         }
         *reinterpret_cast<uint2*>(codes + r * kD) = make_uint2(c[0], c[1]);
         *reinterpret_cast<uint2*>(codes + r * kD + kD / 2) = make_uint2(c[2], c[3]);

@@ -193,6 +193,58 @@ def test_append_zeros_infinities_nan_and_edges():
     assert float(pc.k_scales[b.table[0, 0].long()]) == 2.0 ** -126
 
 
+@pytest.mark.parametrize("rows,page", [(1, 16), (2, 64), (40, 16), (90, 128)])
+def test_append_under_a_callers_own_scales(rows, page):
+    """Pages filled by another quantizer: scales that are no power of two are kept, or grow to one."""
+    b = Batch([rows, rows], [9, 13], 4, 4, page, seed=rows + page, base=300.0)
+    b.scales = [torch.where(torch.arange(s.numel()).view(s.shape) % 3 == 0, s * 0.37, torch.full_like(s, 0.3)) for s in b.scales]
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    nsnq.nsnq_paged_append(b.k.cuda(), b.v.cuda(), pc, table, lens, cu, rope_base=b.base)
+    codes, scales = b.stored()
+    OP.append(b.k.double().numpy(), b.v.double().numpy(), codes, scales, b.table.tolist(), b.lens, b.cu, b.base)
+    check_pool(pc, codes, scales)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 150])
+def test_attention_under_a_callers_own_scales(rows):
+    b = Batch([rows, rows], [300, 77], 8, 2, 16, seed=rows)
+    b.scales = [s * (0.7 + torch.rand(s.shape, generator=torch.Generator().manual_seed(rows))) for s in b.scales]
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=rows)
+    check_out(got, b.q, b, *b.stored())
+
+
+@pytest.mark.parametrize("new,before,hq,hkv", [([1], [600], 64, 1), ([1, 1], [40, 300], 33, 1), ([3, 1], [200, 9], 40, 2)])
+def test_attention_many_heads_to_a_kv_head(new, before, hq, hkv):
+    b = Batch(new, before, hq, hkv, 32, seed=hq)
+    b.tails(0x7F)
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    check_out(nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=max(new)), b.q, b, *b.stored())
+
+
+def test_append_feeds_the_other_attention():
+    """q rotated by the append is read by nsnq_attn_decode, whose kernel may start under its predecessor."""
+    hq, hkv, T = 8, 2, 400
+    b = Batch([1, 1], [20, 33], hq, hkv, 16, seed=98)
+    pc, (table, lens, _) = b.cache(), b.dev()
+    g = torch.Generator(device="cuda").manual_seed(99)
+    cb = nsnq.Codebook(torch.randn(256, 8, generator=g, device="cuda"))
+    caches = [nsnq.Cache.empty(2, hkv, T, 8) for _ in range(2)]
+    for c in caches:
+        nsnq.nsnq_encode(torch.randn(2, hkv, T, D, generator=g, device="cuda"), cb, c)
+    seq = torch.full((2,), T, dtype=torch.int32, device="cuda")
+    k, v, q = b.k.cuda(), b.v.cuda(), b.q.cuda()
+    want = None
+    for i in range(20):
+        q_out = torch.zeros(2, hq, D, dtype=torch.bfloat16, device="cuda")
+        nsnq.nsnq_paged_append(k, v, pc, table, lens, q=q, q_out=q_out, rope_base=b.base)
+        if i == 0:
+            torch.cuda.synchronize()
+        got = nsnq.nsnq_attn_decode(q_out, caches[0], caches[1], cb, cb, seq, T, hkv)
+        want = got if i == 0 else want
+        assert torch.equal(got, want)
+
+
 def test_append_reports_bad_pages_and_lengths():
     b = Batch([20, 3, 2, 4], [3, 40, 1, 7], 2, 2, 16, seed=13)
     b.table[0, 1] = -1
