@@ -14,6 +14,12 @@
 // (about one code in 10^5). The cos and sin of a page's rows are computed once
 // per block, in shared memory, and serve all its heads.
 //
+// What bounds it: memory, in the end (a row is read once and written once; the
+// next heads' rows are copied to shared memory ahead by cp.async). A prompt of
+// 8 x 4096 tokens, 8 kv-heads and 32 query heads, bf16 takes 180 us: 738 MB at
+// 4.1 TB/s (62 % of the measured copy rate). fp64 throughout took 498 us, fp32
+// with one head's rows in flight 311, with the next head's in registers 196.
+//
 #include <math.h>
 
 #include "paged.cuh"
@@ -526,16 +532,19 @@ cudaError_t launch_type(const PagedAppendArgs& a, int64_t grid, cudaStream_t s) 
 
 cudaError_t launch_paged_append(PagedAppendArgs a, bool bf16, cudaStream_t s) {
     // A row or two per sequence: a page block would hold 64 threads and more to
-    // each row it has.
+    // each row it has (64 sequences of one row, 80 heads, pages of 64: 26 us as
+    // page blocks, 12 us as a warp per page and head, both from a cold cache).
     if (a.seqs.n_rows <= 2 * (int64_t)a.seqs.B) return bf16 ? launch_few<__nv_bfloat16>(a, s) : launch_few<float>(a, s);
     // Heads per block: more of them share a page's cos and sin (computing those
-    // costs a block as much as two or three heads), as long as there are blocks
-    // for every SM eight times over.
+    // costs a block as much as two or three heads), as long as there are four
+    // blocks to an SM. Measured with two, four and eight to an SM: 5 sequences x
+    // ~580 rows, fp32 33, 21, 22 us; 2 x 1000 rows 26, 26, 33 us; one of 4096
+    // rows, pages of 128, 67, 61, 73 us.
     int64_t grid = 0;
     for (a.heads = 32;; a.heads /= 2) {
         const int64_t kv = (a.Hkv + a.heads - 1) / a.heads, q = a.q ? (a.Hq + a.heads - 1) / a.heads : 0;
         grid = a.items * (2 * kv + q);
-        if (a.heads == 1 || grid >= 8 * (int64_t)device_sm_count()) break;
+        if (a.heads == 1 || grid >= 4 * (int64_t)device_sm_count()) break;
     }
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     return bf16 ? launch_type<__nv_bfloat16>(a, grid, s) : launch_type<float>(a, grid, s);

@@ -18,11 +18,23 @@
 // 256, elements below 2^-14 of that lose bits to an absolute 2^-24 of it);
 // three hold weights to 2^-12, six hold fp32 queries and weights to 2^-24.
 // Products of codes are exact in fp32, and fp32 is what TMEM accumulates.
+// (The alternative, widening K and V to 16 bits for kind::f16, would write and
+// read every tile once more through shared memory: 64 KB more for the 32 KB
+// that arrive, next to 32 KB that the MMAs read now.)
 //
 // The running maximum m of a row may lag by 2^kLag, so that a tile seldom
 // needs it raised: a vote of the 128 token threads per tile decides; sums of
 // p stay per thread until the segment ends. The bias 2^kBias keeps the
 // smallest piece of a weight at 2^-24 of the row's largest weight.
+//
+// What bounds it: memory for up to 4 rows (16 sequences x 32k tokens, 8
+// kv-heads, 4 query heads each: 166 us, 6.5 TB/s, 98 % of the measured copy
+// rate); one 131k sequence 53 us (5.0 TB/s: start, join and the longer waits of
+// single pages weigh in). With 8 and 16 rows the token warps' work does: 64
+// sequences under a 2048 window, 8 heads 64 us (4.2 TB/s), 13 x 4 drafted rows
+// over ~6k tokens, 4 heads 55 us (2.9 TB/s). A lag of 2^3 instead of 2^5 raised
+// maxima in half of those tiles (69 us). One-CUDA-core-row-per-block attention,
+// the first version, took 6461 us for the 16 x 32k batch.
 #include <math.h>
 
 #include "attn_split.cuh"
@@ -36,10 +48,13 @@ constexpr int kThreads = 192;  // warps 0-3: tokens / channels; 4: TMA; 5: MMA i
 constexpr float kLag = 5.f, kBias = 2.f;  // weights stay below 2^7 (1 + 2^-20)
 constexpr int kShift = 6;                  // bits between the pieces of a weight
 constexpr int kMaxSlots = 8;   // pages per tile (page_size 16)
-constexpr int kSetup = 3;      // tiles that a unit's queries and epilogue cost
+constexpr int kMaxRows = 16;   // of a unit
+// Tiles that a unit's queries and epilogue cost (1, 2, 3: 13 x 4 rows 57.0, 55.3,
+// 55.1 us; 64 windows 65.4, 65.2, 64.3).
+constexpr int kSetup = 3;
 
 constexpr int pad16(int n) { return (n + 15) / 16 * 16; }
-constexpr int pow2_at_least(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
+constexpr int pow2_at_least(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }  // TMEM columns
 
 // RC rows per unit, QP pieces of a query, PP pieces of a weight.
 template <int RC, int QP, int PP>
@@ -58,11 +73,11 @@ struct Misc {
     PagedRange range;
     uint32_t ok[3];               // stage: pages of the tile that were loaded
     float ks[3][kMaxSlots], vs[3][kMaxSlots];
-    float2 cb[32];                // row: score scale (softmax scale, log2 e, query scale); bias - maximum
-    float m[32];                  // row: running maximum (log2 units)
-    int pos[32];                  // row: token position
-    float red[4][33];
-    uint32_t nan[32][4];          // row: channels that a NaN code of a partly seen tile reaches
+    float2 cb[kMaxRows];                // row: score scale (softmax scale, log2 e, query scale); bias - maximum
+    float m[kMaxRows];                  // row: running maximum (log2 units)
+    int pos[kMaxRows];                  // row: token position
+    float red[4][kMaxRows + 1];
+    uint32_t nan[kMaxRows][4];          // row: channels that a NaN code of a partly seen tile reaches
 };
 
 __device__ __forceinline__ uint32_t f16x2(float a, float b) {
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (; walk.live(); walk.next()) {
             const PagedUnit u = walk.u;
             const int j0 = walk.j0, j1 = walk.j1;
-            const uint32_t real = u.rows >= 32 ? kFull : (1u << u.rows) - 1u;
+            const uint32_t real = (1u << u.rows) - 1u;
             bar_tokens();  // the segment before is done with the row data
             write_queries<RC, QP, QT>(a, u, walk.h, sm + Sh::kQ, ms);
             proxy_fence();
@@ -388,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float2 cb = ms.cb[r];
                     z[r] = fmaf(z[r], cb.x, cb.y);
                 }
-                if (vis != kFull) {
+                if (vis != (1u << RC) - 1u) {
 #pragma unroll
                     for (int r = 0; r < RC; ++r) z[r] = (vis >> r) & 1u ? z[r] : -INFINITY;
                 }
@@ -404,10 +419,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (lane == 0) ms.red[warp][r] = top;
                     }
                     const float top_v = warp_max_f32(vis ? vs : 0.f);
-                    if (lane == 0) ms.red[warp][32] = top_v;
+                    if (lane == 0) ms.red[warp][kMaxRows] = top_v;
                     bar_tokens();
-                    const float vn = fmaxf(fmaxf(vref, fmaxf(ms.red[0][32], ms.red[1][32])),
-                                           fmaxf(ms.red[2][32], ms.red[3][32]));
+                    const float vn = fmaxf(fmaxf(vref, fmaxf(ms.red[0][kMaxRows], ms.red[1][kMaxRows])),
+                                           fmaxf(ms.red[2][kMaxRows], ms.red[3][kMaxRows]));
                     const float fv = vref > 0.f ? vref / vn : 0.f;
                     vref = vn;
                     float f[RC];
@@ -566,11 +581,11 @@ cudaError_t launch_cols(const PagedAttnArgs& a, cudaStream_t s) {
 }
 
 // Rows of a unit: the least power of two that holds a sequence's rows of one
-// kv-head; at most 32, and 8 where fp32 takes six pieces of everything.
+// kv-head; at most 16, and 8 where fp32 takes six pieces of everything.
 int unit_rows(int64_t pairs, bool f32) {
     if (pairs <= 4) return 4;
     if (pairs <= 8 || f32) return 8;
-    return pairs <= 16 ? 16 : 32;
+    return 16;
 }
 
 }  // namespace
@@ -579,11 +594,9 @@ size_t paged_attn_workspace(int64_t n_rows, int, int Hq, int Hkv, int64_t max_ro
     const int64_t rows = max_rows < n_rows ? max_rows : n_rows;
     const int rc = unit_rows(rows * (Hq / Hkv), false);
     const int ctas = 2 * device_sm_count();
-    const size_t cols = rc <= 8    ? paged_workspace<8>(ctas)
-                        : rc == 16 ? paged_workspace<16>(ctas)
-                                   : paged_workspace<32>(ctas);
+    const size_t cols = rc <= 8 ? paged_workspace<8>(ctas) : paged_workspace<16>(ctas);
     const size_t whole = paged_rows_workspace();
-    return rows * (Hq / Hkv) > 32 && whole > cols ? whole : cols;
+    return rows * (Hq / Hkv) > kMaxRows && whole > cols ? whole : cols;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
@@ -595,12 +608,15 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
             return rc == 4 ? launch_cols<4, 2, 6, __nv_bfloat16>(a, s) : launch_cols<8, 2, 6, __nv_bfloat16>(a, s);
         return rc == 4 ? launch_cols<4, 6, 6, float>(a, s) : launch_cols<8, 6, 6, float>(a, s);
     }
-    if (rows * (a.Hq / a.Hkv) > 32) return launch_paged_rows(a, s);
+    // More rows than a unit here takes go to 256-row units on their own kernel. A
+    // variant of this one for 32 rows took as long or longer: 8 sequences of 8k
+    // tokens, 20 and 32 rows per kv-head, 84.5 and 92.1 us against 85.5 and 87.8;
+    // 40 of 500 tokens, 32 rows, 71 against 60 us.
+    if (rows * (a.Hq / a.Hkv) > kMaxRows) return launch_paged_rows(a, s);
     switch (rc) {
         case 4: return launch_cols<4, 2, 3, __nv_bfloat16>(a, s);
         case 8: return launch_cols<8, 2, 3, __nv_bfloat16>(a, s);
-        case 16: return launch_cols<16, 2, 3, __nv_bfloat16>(a, s);
-        default: return launch_cols<32, 2, 3, __nv_bfloat16>(a, s);
+        default: return launch_cols<16, 2, 3, __nv_bfloat16>(a, s);
     }
 }
 

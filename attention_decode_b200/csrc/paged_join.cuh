@@ -64,7 +64,7 @@ constexpr int kMaxParts = 640;  // CTAs of the largest grid (two per SM of up to
 // token.
 template <int RC>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
-    constexpr int kWarps = kJoinThreads / 32, kShare = RC <= 32 ? kWarps : 1;  // warps to a row
+    constexpr int kWarps = kJoinThreads / 32, kShare = RC <= 16 ? kWarps : 1;  // warps to a row
     __shared__ float factor[kWarps][kMaxParts / kShare + 1];
     __shared__ float4 sums[kWarps][32];
     const int lane = lane_id(), warp = threadIdx.x >> 5;
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 template <int RC>
 cudaError_t launch_paged_join(const PagedAttnArgs& a, int grid, cudaStream_t s) {
     static std::atomic<unsigned long long> ready{0};
-    return launch_smem_pdl(paged_join_kernel<RC>, ready, dim3(grid + a.seqs.B, RC <= 32 ? RC : RC / 4), dim3(kJoinThreads), 0, s, a,
+    return launch_smem_pdl(paged_join_kernel<RC>, ready, dim3(grid + a.seqs.B, RC <= 16 ? RC : RC / 4), dim3(kJoinThreads), 0, s, a,
                            grid);
 }
 

@@ -13,10 +13,20 @@
 // fp16 weights keep 11 bits; the running maximum may lag by 2^kLag and the
 // bias 2^kBias keeps the largest below 2^15 and the smallest at 2^-27.
 //
-// What bounds it: the tensor cores (2 x 512 clocks per half and tile) and the
-// exponentials (16384 per half and tile, 16 a clock: 1024 clocks). The halves
-// take turns: while one half's weights are computed, the tensor cores work
-// for the other (P V of the tile before, then S of the next).
+// What bounds it: a tile needs 2048 clocks of the tensor cores (2 halves x (S
+// 512 + P V 512)) and 2048 of the exponential unit (2 x 16384 at 16 a clock), and
+// takes ~4900: each is busy 40 % of the time, the issue slots 50 %. A row warp's
+// own chain (scores from TMEM, exponents, weights back, 64 tokens at a time) is
+// 1840 clocks long where the exponential unit alone would allow 512, and an SM
+// sub-partition has two such warps. Measured: a prompt of 8192 tokens, 32 query
+// heads on 8 kv-heads, causal, 713 us (771 TFLOP/s, 47 % of the measured bf16
+// rate); 447 + 280 rows behind 21.5k and 16.8k tokens 305 us (774 TFLOP/s);
+// 4 prompts of ~1500 under a 511 window with 5 sinks 146 us. On the way: scores
+// in one go per tile 929 us, then 64-token steps with the next scores in flight
+// and MMA issue under elect (before, the issuing thread alone took 1700 clocks
+// per half and step) 749 us. Tried: two threads per row (794 us with, 822
+// without a register split; the second barrier per step and spills cost what
+// the overlap gains), the scores of the next chunk loaded ahead (735-760 us).
 #include <math.h>
 
 #include "f32x2.cuh"
@@ -31,7 +41,9 @@ constexpr int kThreads = 512;   // warps 0-3, 4-7: rows; 8-11: V to fp16; 12: TM
 constexpr float kLag = 12.f, kBias = 3.f;
 constexpr int kKStages = 3, kRing = 8;
 constexpr int kMaxSlots = 8;
-constexpr int kSetup = 5;       // tiles that a unit's queries and epilogue cost
+// Tiles that a unit's queries and epilogue cost (2, 3, 5, 8: the 8192 prompt 795,
+// 733, 689, 695 us; short windows 143, 144, 147, 148 us).
+constexpr int kSetup = 5;
 
 // shared memory, from a 1024-aligned base
 constexpr uint32_t kQ = 0;                        // [half][piece][128 rows][128 B]
