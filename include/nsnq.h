@@ -445,9 +445,10 @@ typedef enum {
  * that holds older tokens of the sequence keep its scale if they fit under
  * it; else the scale grows and the page's older codes are rounded again to
  * the new one (exact but for codes that fall below e4m3's normal range).
- * Rows behind the new tokens are left as they were. Pages that several
- * sequences of a call write to are the caller's error (their contents are
- * then any mix of both).
+ * Rows behind the new tokens are left as they were, and so are q_out rows of
+ * sequences reported as NSNQ_PAGED_BAD_LENGTH. Pages that several sequences
+ * of a call write to are the caller's error (their contents are then any mix
+ * of both).
  * B, Hq, Hkv <= 65535, n_rows * max(Hq, Hkv) < 2^31 (NSNQ_ERR_UNSUPPORTED
  * above). Hkv must equal cache.heads. n_rows = 0 or B = 0 is a no-op.
  */
@@ -483,7 +484,11 @@ size_t nsnq_paged_attn_workspace(int64_t n_rows, int B, int Hq, int Hkv, int D, 
  * not see never change its result, whatever their bits (NaN codes too).
  * Query head h reads kv-head h / (Hq / Hkv). cu_rows, seq_lens, page_table
  * and the limits are those of nsnq_paged_append; every value of the cache's
- * scales must be finite and positive.
+ * scales must be finite and positive (powers of two or not).
+ * Scores and sums are fp32. With bf16 q and out, weights p are rounded to 11
+ * bits or more, and weights below 2^-24 of a row's largest may vanish; with
+ * fp32 q or out, queries and weights keep 24 bits, at a several times lower
+ * rate for prompts. The same call gives the same bits every time.
  */
 nsnq_status nsnq_paged_attn(const void* q, nsnq_dtype q_dtype, int64_t n_rows, int64_t q_stride_t,
                             int64_t q_stride_h, const int32_t* cu_rows, int64_t max_rows,
