@@ -68,7 +68,7 @@ struct Shape {
 };
 
 struct Misc {
-    uint64_t full[3], empty[3], s_full[2], s_free[2], p_full[2], p_free[2], q_ready;
+    uint64_t full[3], empty[3], s_full[2], s_free[2], p_full[2], p_free[2], q_ready, done;
     uint32_t tmem;
     PagedRange range;
     uint32_t ok[3];               // stage: pages of the tile that were loaded
@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(smem_u32(&ms.p_free[i]), 1);
         }
         mbar_init(smem_u32(&ms.q_ready), 4);
+        mbar_init(smem_u32(&ms.done), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tmem_alloc(smem_u32(&ms.tmem), Sh::kTmem);
@@ -309,9 +310,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
         if (missing) paged_report(a.seqs, kBadPage);
+        // No copy is in flight at the end, not even after a wait that failed.
 #pragma unroll 1
-        for (uint32_t i = it < ST ? 0 : it - ST; i < it; ++i)  // no copy is in flight at the end
-            wait(smem_u32(&ms.full[i % ST]), (i / ST) & 1);
+        for (uint32_t i = it < ST ? 0 : it - ST; i < it; ++i) mbar_wait(smem_u32(&ms.full[i % ST]), (i / ST) & 1);
     } else if (warp == 5) {
         // ------------------------------------------------------------ MMA --
         if (elect_one()) {
@@ -351,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 it += cnt;
             }
+            mma_commit(smem_u32(&ms.done));  // nor an MMA
+            mbar_wait(smem_u32(&ms.done), 0);
         }
         __syncwarp();
     } else {

@@ -54,7 +54,7 @@ constexpr uint32_t kMisc = kV16 + 4 * 16384;
 
 struct Misc {
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2], w_full[2], w_free[2], sc_full[kRing];
-    uint64_t q_ready[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2];
+    uint64_t q_ready[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], done;
     uint32_t tmem;
     PagedRange range;
     uint32_t ok[kRing];                // pages of the tile that were loaded
@@ -161,6 +161,7 @@ struct RowState {
 // if there is one, its output by a factor.
 __device__ __noinline__ void rescale_row(uint32_t s, int done, uint32_t o, bool have_o, float f) {
     const uint32_t f2 = f16x2(f, f);
+    tmem_wait_st();  // the weights so far may still be on their way
 #pragma unroll 1
     for (int i = 0; i < done; i += 8) {
         uint32_t u[8];
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ms.o_full[i]), 1);
         }
         for (int i = 0; i < kRing; ++i) mbar_init(smem_u32(&ms.sc_full[i]), 33);
+        mbar_init(smem_u32(&ms.done), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tmem_alloc(smem_u32(&ms.tmem), 512);
@@ -375,11 +377,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (missing) paged_report(a.seqs, kBadPage);
+        // No copy is in flight at the end, not even after a wait that failed.
 #pragma unroll 1
-        for (uint32_t i = it < 3 ? 0 : it - 3; i < it; ++i)  // no copy is in flight at the end
-            wait(smem_u32(&ms.k_full[i % kKStages]), (i / kKStages) & 1);
+        for (uint32_t i = it < 3 ? 0 : it - 3; i < it; ++i)
+            mbar_wait(smem_u32(&ms.k_full[i % kKStages]), (i / kKStages) & 1);
 #pragma unroll 1
-        for (uint32_t i = it < 2 ? 0 : it - 2; i < it; ++i) wait(smem_u32(&ms.v_full[i & 1]), (i >> 1) & 1);
+        for (uint32_t i = it < 2 ? 0 : it - 2; i < it; ++i) mbar_wait(smem_u32(&ms.v_full[i & 1]), (i >> 1) & 1);
         } else if (warp == 13) {
         // ------------------------------------------------------------ MMA --
         if (elect_one()) {
@@ -433,6 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 it += cnt >> 1;
             }
+            mma_commit(smem_u32(&ms.done));  // nor an MMA
+            mbar_wait(smem_u32(&ms.done), 0);
         }
         __syncwarp();
         }

@@ -568,6 +568,53 @@ def test_two_streams_and_repeats(rows):
         assert all(torch.equal(g, want[i]) for g in got[i])
 
 
+@pytest.mark.parametrize("rows", [1, 200])
+def test_two_captured_calls_at_once(rows):
+    """Two captured calls, their workspaces allocated in the capture, replayed on two streams at once."""
+    b = [Batch([rows] * 3, [700, 33, 250], 8, 2, 32, seed=191 + i) for i in range(2)]
+    sides = []
+    for x in b:
+        pc, dev, q = x.cache(), x.dev(), x.q.cuda()
+        want = nsnq.nsnq_paged_attn(q, pc, *dev, max_rows=rows)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = nsnq.nsnq_paged_attn(q, pc, *dev, max_rows=rows)
+        sides.append((graph, out, want, torch.cuda.Stream(), (pc, dev, q)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for graph, out, _, stream, _ in sides:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (graph, out, want, _, _), x in zip(sides, b):
+        assert torch.equal(out, want)
+        check_out(out, x.q, x, *x.stored())
+    del sides
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_pool_of_more_than_32_bits(rows):
+    """Pages whose bytes lie past 4 GiB: the same codes, scales and outputs as in a small pool."""
+    b = Batch([rows, rows], [300, 0], 8, 8, 128, seed=195)
+    pages = len(b.codes[0])
+    small, (table, lens, cu) = b.cache(), b.dev()
+    q, k, v = b.q.cuda(), b.k.cuda(), b.v.cuda()
+    big = nsnq.PagedCache.empty(33000, 8, 128)
+    far = 33000 - pages
+    assert far * 8 * 128 * D > 1 << 32
+    for x, y in ((big.k, small.k), (big.v, small.v)):
+        x[far:].view(torch.uint8).copy_(y.view(torch.uint8))
+    big.k_scales[far:], big.v_scales[far:] = small.k_scales, small.v_scales
+    outs = []
+    for pc, t in ((small, table), (big, table + far)):
+        qr = nsnq.nsnq_paged_append(k, v, pc, t, lens, cu, q=q, rope_base=b.base)
+        outs.append(nsnq.nsnq_paged_attn(qr, pc, t, lens, cu, max_rows=rows))
+    assert torch.equal(*outs)
+    for x, y in ((big.k, small.k), (big.v, small.v)):
+        assert torch.equal(x[far:].view(torch.uint8), y.view(torch.uint8))
+    assert torch.equal(big.k_scales[far:], small.k_scales) and torch.equal(big.v_scales[far:], small.v_scales)
+
+
 def test_shared_prefix_pages_and_table_stride():
     """Two sequences over the same prefix pages; the table a slice of a wider one."""
     b = Batch([1, 1], [127, 140], 8, 2, 32, seed=95)
