@@ -137,6 +137,21 @@ def test_append_many_sequences_without_cu(page):
     check_pool(pc, codes, scales)
 
 
+@pytest.mark.parametrize("count", [33, 1025, 2050])
+def test_append_few_rows_of_many_sequences(count):
+    """0, 1, 2 and more rows a sequence, two on average: every row finds its sequence."""
+    new = [(0, 1, 2, 0, 5, 1, 2)[i % 7] for i in range(count)]
+    b = Batch(new, [(29 * i) % 47 for i in range(count)], 1, 1, 16, seed=count)
+    assert sum(new) <= 2 * count
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    got = nsnq.nsnq_paged_append(b.k.cuda(), b.v.cuda(), pc, table, lens, cu, q=b.q.cuda(), rope_base=b.base)
+    codes, scales = b.stored()
+    OP.append(b.k.double().numpy(), b.v.double().numpy(), codes, scales, b.table.tolist(), b.lens, b.cu, b.base)
+    check_pool(pc, codes, scales)
+    check_rotated(got, b.q, b)
+    pc.check()
+
+
 def test_append_strides_and_in_place_queries():
     """Rows of a fused projection [rows][(Hq + 2 Hkv) D], heads of a [heads][rows] layout, q rotated in place."""
     b = Batch([6, 11], [20, 3], 4, 2, 16, seed=5)
