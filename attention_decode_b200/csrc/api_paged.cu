@@ -113,9 +113,8 @@ nsnq_status nsnq_paged_append(const void* k, const void* v, const void* q, void*
     a.rope = rope_base != 0.0;
     a.kc = cache.k; a.vc = cache.v; a.ks = cache.k_scales; a.vs = cache.v_scales;
     a.num_pages = cache.num_pages; a.page = cache.page_size;
-    // a sequence of n rows touches at most n / page + 2 pages, and at most n
-    const int64_t most = n_rows / a.page + 2 * (int64_t)B;
-    a.items = n_rows < most ? n_rows : most;
+    // a sequence of n rows touches at most n / page + 2 pages
+    a.items = n_rows / a.page + 2 * (int64_t)B;
     for (int i = 0; i < D / 2 && a.rope; ++i) {
         a.freq[i] = pow(rope_base, -2.0 * i / D);
         a.turns[i] = a.freq[i] / 6.283185307179586476925;

@@ -152,6 +152,21 @@ def test_append_few_rows_of_many_sequences(count):
     pc.check()
 
 
+@pytest.mark.parametrize("count,page", [(2, 16), (33, 16), (33, 128), (1100, 32)])
+def test_append_rows_of_many_sequences(count, page):
+    """More than two rows a sequence on average, some with none, some over three pages."""
+    new = [(0, 7, 2, 2 * page + 1, 1, 0, page)[(i + 3) % 7] for i in range(count)]
+    b = Batch(new, [(29 * i) % (page + 3) for i in range(count)], 1, 1, page, seed=count)
+    assert sum(new) > 2 * count
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    got = nsnq.nsnq_paged_append(b.k.cuda(), b.v.cuda(), pc, table, lens, cu, q=b.q.cuda(), rope_base=b.base)
+    codes, scales = b.stored()
+    OP.append(b.k.double().numpy(), b.v.double().numpy(), codes, scales, b.table.tolist(), b.lens, b.cu, b.base)
+    check_pool(pc, codes, scales)
+    check_rotated(got, b.q, b)
+    pc.check()
+
+
 def test_append_strides_and_in_place_queries():
     """Rows of a fused projection [rows][(Hq + 2 Hkv) D], heads of a [heads][rows] layout, q rotated in place."""
     b = Batch([6, 11], [20, 3], 4, 2, 16, seed=5)
