@@ -11,8 +11,8 @@
 // and every piece is a column of its own. The scores of a tile are
 //   S[token][piece, row] = K q^T   (M = 128 tokens, N = pieces x rows, K = 128 channels),
 // lane t of TMEM holding token t; a thread adds its token's pieces, applies
-// the page's scale, takes p = 2^(s - m), and writes w = p * (v scale / the
-// segment's largest v scale) in pieces; then
+// the page's scale, takes p = 2^(s - m), and writes w = p * v scale / 2^e in
+// pieces, e the row's own (below); then
 //   O[channel][piece, row] += V^T w   (M = 128 channels, K = 128 tokens).
 // Two pieces hold a bf16 query exactly (8 bits; the row scaled to at most
 // 256, elements below 2^-14 of that lose bits to an absolute 2^-24 of it);
@@ -24,8 +24,13 @@
 //
 // The running maximum m of a row may lag by 2^kLag, so that a tile seldom
 // needs it raised: a vote of the 128 token threads per tile decides; sums of
-// p stay per thread until the segment ends. The bias 2^kBias keeps the
-// smallest piece of a weight at 2^-24 of the row's largest weight.
+// p stay per thread until the segment ends. A second maximum per row, with the
+// same lag, is that of log2 p + log2 v scale; its distance from the first one, in
+// whole powers of two, is the e of w, so that w spans the pieces' range whatever
+// the scales are. The bias 2^kBias keeps the smallest piece at 2^-23 of the row's
+// largest w. Where every row's 2^e is the token's v scale (equal scales, powers of
+// two), w is p. A row's maxima move only for tokens that it sees itself: no bit of
+// a row depends on what it does not see.
 //
 // What bounds it: memory for up to 4 rows (16 sequences x 32k tokens, 8
 // kv-heads, 4 query heads each: 166 us, 6.5 TB/s, 98 % of the measured copy
@@ -73,10 +78,15 @@ struct Misc {
     PagedRange range;
     uint32_t ok[3];               // stage: pages of the tile that were loaded
     float ks[3][kMaxSlots], vs[3][kMaxSlots];
-    float2 cb[kMaxRows];                // row: score scale (softmax scale, log2 e, query scale); bias - maximum
-    float m[kMaxRows];                  // row: running maximum (log2 units)
+    float qs[kMaxRows];                 // row: score scale (softmax scale, log2 e, query scale)
     int pos[kMaxRows];                  // row: token position
-    float red[4][kMaxRows + 1];
+    // each warp's own copy, for row: score scale, bias - maximum; 2^-e and -e, w = p * v scale * 2^-e
+    float2 cb[4][kMaxRows];
+    alignas(16) float rv[4][kMaxRows];
+    alignas(16) float lrv[4][kMaxRows];
+    float2 factor[4][kMaxRows];         // as a row's maxima rise: of its sum of weights, of its outputs
+    float2 red[4][kMaxRows];            // a warp's tokens: largest score, largest score + log2 v scale
+    float sums[4][kMaxRows];
     uint32_t nan[kMaxRows][4];          // row: channels that a NaN code of a partly seen tile reaches
 };
 
@@ -117,6 +127,31 @@ __device__ __forceinline__ void weight_pieces(float w0, float w1, uint32_t (&out
     }
 }
 
+// The weights of a token from their exponents z, added to the rows' sums l, and
+// the pieces of what meets the values. ONE: for every token of the warp that is
+// the weight itself; else only where vs = 0.
+template <int RC, int PP, bool ONE>
+__device__ __forceinline__ void weigh(const float* rv, const float (&z)[RC], float vs, float (&l)[RC],
+                                      uint32_t (&word)[pad16(RC * PP) / 4]) {
+#pragma unroll
+    for (int i = 0; i < pad16(RC * PP) / 4; ++i) word[i] = 0;
+#pragma unroll
+    for (int r = 0; r < RC; r += 2) {
+        float w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            w[i] = exp2_approx(z[r + i]);
+            l[r + i] += w[i];
+            // (2^-e first: finite next to the largest scale, and a weight of 0 stays 0)
+            if (!ONE) w[i] = vs != 0.f ? w[i] * rv[r + i] * vs : w[i];
+        }
+        uint32_t c[PP];
+        weight_pieces<PP>(w[0], w[1], c);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) word[(k * RC + r) / 4] |= c[k] << (((k * RC + r) & 2) * 8);
+    }
+}
+
 __device__ __forceinline__ void bar_tokens() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool any_token(bool v) {  // vote of the 128 token threads
     uint32_t r;
@@ -152,6 +187,57 @@ __device__ __forceinline__ float warp_max_f32(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
+}
+
+__device__ __forceinline__ float power_of_two(float e) {  // of a whole number e from -126 to 127
+    return __uint_as_float((uint32_t)((int)e + 127) << 23);
+}
+
+// The rows' state of a segment, kept by every warp alike: lane l has row l % RC's
+// maximum m (log2 units) and exponent -e.
+struct RowState {
+    float m, lrv;
+    float v_one;    // the v scale under which every row's w is p (0: none)
+    float lrv_top;  // the largest -e of a row that has seen a token
+};
+template <int RC>
+__device__ __forceinline__ RowState first_state(Misc& ms, int warp, int rows) {
+    const int r = lane_id() % RC;
+    ms.cb[warp][r] = make_float2(ms.qs[r], r < rows ? INFINITY : kBias);
+    ms.rv[warp][r] = 1.f;
+    ms.lrv[warp][r] = 0.f;
+    __syncwarp();
+    return {r < rows ? -INFINITY : 0.f, 0.f, 0.f, 0.f};
+}
+// Rows' maxima raised to the tile's (ms.red) where the tile passes a lag. The e is the whole number below the
+// distance of the maxima (a little above it, for the rounding of their sum), so
+// that the largest w is between 2^kBias and twice that; its bounds keep p * 2^-e
+// finite.
+template <int RC>
+__device__ __forceinline__ void raise_maxima(Misc& ms, int warp, RowState& st) {
+    const int r = lane_id() % RC;
+    const float top = fmaxf(fmaxf(ms.red[0][r].x, ms.red[1][r].x), fmaxf(ms.red[2][r].x, ms.red[3][r].x));
+    const float top_w = fmaxf(fmaxf(ms.red[0][r].y, ms.red[1][r].y), fmaxf(ms.red[2][r].y, ms.red[3][r].y));
+    const bool need = top - st.m > kLag || top_w - st.m + st.lrv > kLag;
+    const float mn = need ? fmaxf(st.m, top) : st.m, e0 = -st.lrv;
+    const float e = need ? fminf(fmaxf(floorf(fmaxf(st.m + e0, top_w) - mn + 0.0625f), -118.f), 126.f) : e0;
+    const float down = st.m == mn ? 0.f : st.m - mn;
+    ms.factor[warp][r] = make_float2(exp2_approx(down), exp2_approx(down + (e0 - e)));
+    st.m = mn;
+    st.lrv = -e;
+    ms.cb[warp][r].y = kBias - mn;
+    ms.rv[warp][r] = power_of_two(st.lrv);
+    ms.lrv[warp][r] = st.lrv;
+    __syncwarp();
+}
+// The same for every row: v_one and lrv_top.
+template <int RC>
+__device__ __forceinline__ void sum_up(RowState& st, int rows) {
+    const bool seen = lane_id() % RC < rows && st.m > -INFINITY;
+    const unsigned who = __ballot_sync(kFull, seen);
+    const float first = __shfl_sync(kFull, st.lrv, who ? __ffs(who) - 1 : 0);
+    st.v_one = __all_sync(kFull, !seen || st.lrv == first) ? power_of_two(-first) : 0.f;
+    st.lrv_top = warp_max_f32(seen ? st.lrv : -INFINITY);
 }
 
 template <int RC, int QP, typename QT>
@@ -197,9 +283,8 @@ __device__ __forceinline__ void write_queries(const PagedAttnArgs& a, const Page
             *reinterpret_cast<uint32_t*>(q_sm + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4) = word;
         }
         if (lane == 0) {
-            ms.cb[r] = make_float2(a.scale_log2 * down, r < u.rows ? INFINITY : kBias);
+            ms.qs[r] = a.scale_log2 * down;
             ms.pos[r] = pos;
-            ms.m[r] = r < u.rows ? -INFINITY : 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) ms.nan[r][k] = 0u;
         }
@@ -372,7 +457,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready));
             bar_tokens();
-            float l[RC], vref = 0.f;
+            RowState state = first_state<RC>(ms, warp, u.rows);
+            const float2* row_cb = ms.cb[warp];
+            float l[RC];
 #pragma unroll
             for (int r = 0; r < RC; ++r) l[r] = 0.f;
 #pragma unroll 1
@@ -403,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 row_scores<RC, QP>(lanes + buf * N1, ks, z);
 #pragma unroll
                 for (int r = 0; r < RC; ++r) {
-                    const float2 cb = ms.cb[r];
+                    const float2 cb = row_cb[r];
                     z[r] = fmaf(z[r], cb.x, cb.y);
                 }
                 if (vis != (1u << RC) - 1u) {
@@ -413,30 +500,34 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float most = z[0];
 #pragma unroll
                 for (int r = 1; r < RC; ++r) most = fmaxf(most, z[r]);
-                if (any_token(most > kBias + kLag || (vis != 0 && vs > vref))) {
-                    // raise the maxima: per row over the tile's tokens, and the v scale
+                bool over = most > kBias + kLag;
+                if (vis != 0 && vs != state.v_one) {  // some row's w may be too large where its p is not
+                    const float lvs = __log2f(vs);
+                    if (most + lvs + state.lrv_top > kBias + kLag) {
+#pragma unroll
+                        for (int r = 0; r < RC; ++r) over |= z[r] + (lvs + ms.lrv[warp][r]) > kBias + kLag;
+                    }
+                }
+                if (any_token(over)) {
+                    // raise the maxima: per row over the tile's tokens
+                    const float lvs = __log2f(vs), vs0 = __shfl_sync(kFull, vs, 0);
+                    const bool alike = __all_sync(kFull, vis == 0 || vs == vs0);
                     row_scores<RC, QP>(lanes + buf * N1, ks, z);
 #pragma unroll
                     for (int r = 0; r < RC; ++r) {
-                        const float top = warp_max_f32((vis >> r) & 1u ? z[r] * ms.cb[r].x : -INFINITY);
-                        if (lane == 0) ms.red[warp][r] = top;
+                        const float x = (vis >> r) & 1u ? z[r] * row_cb[r].x : -INFINITY, top = warp_max_f32(x);
+                        const float top_w = alike ? top + lvs : warp_max_f32((vis >> r) & 1u ? x + lvs : -INFINITY);
+                        if (lane == 0) ms.red[warp][r] = make_float2(top, top_w);
                     }
-                    const float top_v = warp_max_f32(vis ? vs : 0.f);
-                    if (lane == 0) ms.red[warp][kMaxRows] = top_v;
-                    bar_tokens();
-                    const float vn = fmaxf(fmaxf(vref, fmaxf(ms.red[0][kMaxRows], ms.red[1][kMaxRows])),
-                                           fmaxf(ms.red[2][kMaxRows], ms.red[3][kMaxRows]));
-                    const float fv = vref > 0.f ? vref / vn : 0.f;
-                    vref = vn;
+                    bar_tokens();  // (red is written again behind the next vote at the earliest)
+                    raise_maxima<RC>(ms, warp, state);
                     float f[RC];
 #pragma unroll
                     for (int r = 0; r < RC; ++r) {
-                        const float2 cb = ms.cb[r];
-                        const float mn = fmaxf(fmaxf(ms.m[r], fmaxf(ms.red[0][r], ms.red[1][r])),
-                                               fmaxf(ms.red[2][r], ms.red[3][r]));
-                        f[r] = ms.m[r] == mn ? 1.f : exp2_approx(ms.m[r] - mn);
-                        l[r] *= f[r];
-                        z[r] = (vis >> r) & 1u ? fmaf(z[r], cb.x, kBias - mn) : -INFINITY;
+                        const float2 cb = row_cb[r], by = ms.factor[warp][r];
+                        l[r] *= by.x;
+                        f[r] = by.y;
+                        z[r] = (vis >> r) & 1u ? fmaf(z[r], cb.x, cb.y) : -INFINITY;
                     }
                     if (j > j0) {
                         wait(smem_u32(&ms.p_free[buf ^ 1]), ((it - 1) >> 1) & 1);
@@ -446,41 +537,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                             float v[8];
                             tmem_ld<8>(lanes + 2 * N1 + c0, v);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] *= f[(c0 + i) % RC] * fv;
+                            for (int i = 0; i < 8; ++i) v[i] *= f[(c0 + i) % RC];
                             tmem_st8(lanes + 2 * N1 + c0, v);
                         }
                         tmem_wait_st();
                     }
-                    bar_tokens();
-                    if (tid < RC) {
-                        const float mn = fmaxf(fmaxf(ms.m[tid], fmaxf(ms.red[0][tid], ms.red[1][tid])),
-                                               fmaxf(ms.red[2][tid], ms.red[3][tid]));
-                        ms.m[tid] = mn;
-                        ms.cb[tid].y = kBias - mn;
-                    }
-                    bar_tokens();
+                    sum_up<RC>(state, u.rows);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms.s_free[buf]));
-                const float wv = vis && vref > 0.f ? vs / vref : 0.f;
+                const bool one = vis == 0 || vs == state.v_one;  // w is p
                 uint32_t word[N2 / 4];
-#pragma unroll
-                for (int i = 0; i < N2 / 4; ++i) word[i] = 0;
-#pragma unroll
-                for (int r = 0; r < RC; r += 2) {
-                    float w[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        w[i] = exp2_approx(z[r + i]);
-                        l[r + i] += w[i];
-                        w[i] *= wv;
-                    }
-                    uint32_t c[PP];
-                    weight_pieces<PP>(w[0], w[1], c);
-#pragma unroll
-                    for (int k = 0; k < PP; ++k) word[(k * RC + r) / 4] |= c[k] << (((k * RC + r) & 2) * 8);
-                }
+                if (__all_sync(kFull, one)) weigh<RC, PP, true>(ms.rv[warp], z, 0.f, l, word);
+                else weigh<RC, PP, false>(ms.rv[warp], z, one ? 0.f : vs, l, word);
                 wait(smem_u32(&ms.p_free[buf]), ((it >> 1) & 1) ^ 1);
 #pragma unroll
                 for (int i = 0; i < N2 / 16; ++i)
@@ -526,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int r = 0; r < RC; ++r) {
                 const float s = warp_sum(l[r]);
-                if (lane == 0) ms.red[warp][r] = s;
+                if (lane == 0) ms.sums[warp][r] = s;
             }
             wait(smem_u32(&ms.p_free[(it - 1) & 1]), ((it - 1) >> 1) & 1);
             tc_fence_after();
@@ -550,16 +620,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int r = 0; r < RC; ++r) {
                 if (r >= u.rows) continue;
-                const float sum = ms.red[0][r] + ms.red[1][r] + ms.red[2][r] + ms.red[3][r];
-                float v = o[r] * vref;
+                const float m = __shfl_sync(kFull, state.m, r), vref = power_of_two(-__shfl_sync(kFull, state.lrv, r));
+                const float sum = ms.sums[0][r] + ms.sums[1][r] + ms.sums[2][r] + ms.sums[3][r];
+                float v = o[r];
                 if ((ms.nan[r][tid >> 5] >> (tid & 31)) & 1u) v = NAN;
                 if (!complete) {
-                    part[r * kD + tid] = v;
-                    if (tid == 0) part[RC * kD + r] = ms.m[r], part[RC * kD + RC + r] = sum;
+                    part[r * kD + tid] = v * vref;
+                    if (tid == 0) part[RC * kD + r] = m, part[RC * kD + RC + r] = sum;
                     continue;
                 }
                 const int rr = u.r0 + r, i = (int)fdiv((uint32_t)rr, a.G);
-                store_out(a, (int64_t)(u.row0 + i) * a.Hq + walk.h * G + rr - i * G, tid, sum == 0.f ? 0.f : v / sum);
+                store_out(a, (int64_t)(u.row0 + i) * a.Hq + walk.h * G + rr - i * G, tid, sum == 0.f ? 0.f : v / sum * vref);
             }
         }
     }

@@ -11,7 +11,13 @@
 //   O += P V       kind::f16, P from TMEM (over S), V widened to fp16 (exact)
 //                  in shared memory by a warpgroup of its own.
 // fp16 weights keep 11 bits; the running maximum may lag by 2^kLag and the
-// bias 2^kBias keeps the largest below 2^15 and the smallest at 2^-27.
+// bias 2^kBias keeps the largest below 2^15.75 and steps at 2^-23 of the largest.
+// What meets V's codes is a weight times its page's v scale, over a reference
+// of the row's own: the largest such product among the tokens that the row has
+// seen has a reference of its own lag and takes the range of fp16 as above,
+// whatever the scales are; the sum of the weights stays on their own maximum. A
+// row's maximum and reference move only for its own tokens, so no bit of a row
+// depends on what it does not see.
 //
 // What bounds it: a tile needs 2048 clocks of the tensor cores (2 halves x (S
 // 512 + P V 512)) and 2048 of the exponential unit (2 x 16384 at 16 a clock), and
@@ -38,7 +44,7 @@ namespace {
 
 constexpr int RC = 256;         // rows of a unit
 constexpr int kThreads = 512;   // warps 0-3, 4-7: rows; 8-11: V to fp16; 12: TMA; 13: MMA issue
-constexpr float kLag = 12.f, kBias = 3.f;
+constexpr float kLag = 16.75f, kBias = -1.f, kMost = 55108.f;  // kMost = 2^(kBias + kLag)
 constexpr int kKStages = 3, kRing = 8;
 constexpr int kMaxSlots = 8;
 // Tiles that a unit's queries and epilogue cost (2, 3, 5, 8: the 8192 prompt 795,
@@ -154,42 +160,47 @@ struct View {
 struct RowState {
     float c;           // score scale (softmax scale, log2 e, query scale)
     float m, l;        // running maximum (log2 units), sum of 2^(s - m + kBias)
-    float vref, rv;    // largest v scale so far and its reciprocal
+    float vref;        // reference of weight x v scale, relative to m; 0 before the first token
 };
+
+// The factor of a weight under a page's v scale. (A finite one: a weight of 0
+// stays 0. One that this holds down has passed kLag and raises the reference.)
+__device__ __forceinline__ float value_factor(float vs, const RowState& st) {
+    return vs == st.vref ? 1.f : fminf(__fdividef(vs, st.vref), 0x1p126f);
+}
 
 // Multiplies a row's weights of the step so far (`done` columns of fp16 pairs) and,
 // if there is one, its output by a factor.
 __device__ __noinline__ void rescale_row(uint32_t s, int done, uint32_t o, bool have_o, float f) {
-    const uint32_t f2 = f16x2(f, f);
     tmem_wait_st();  // the weights so far may still be on their way
 #pragma unroll 1
     for (int i = 0; i < done; i += 8) {
         uint32_t u[8];
         TmemLoad<8>::run(s + i, u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) asm("mul.f16x2 %0, %1, %2;" : "=r"(u[k]) : "r"(u[k]), "r"(f2));
+        for (int k = 0; k < 8; ++k) u[k] = f16x2(f16_lo(u[k]) * f, f16_hi(u[k]) * f);
         tmem_st8(s + i, reinterpret_cast<float*>(u));
     }
 #pragma unroll 1
-    for (int i = 0; have_o && i < kD; i += 16) {
-        uint32_t u[16];
-        TmemLoad<16>::run(o + i, u);
+    for (int i = 0; have_o && i < kD; i += 32) {
+        uint32_t u[32];
+        TmemLoad<32>::run(o + i, u);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f);
-        tmem_st16(o + i, u);
+        for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f);
+        tmem_st32(o + i, u);
     }
     tmem_wait_st();
 }
 
 // Weights of 16 columns of a row from their scores u: exponents, the largest
-// of them, 2^x, their sum; packed in fp16 pairs. WEIGH: some page's v scale is
-// not the largest so far. (Exponents are formed in packed pairs, as the scores
+// of them, 2^x, their sum; packed in fp16 pairs, times w. WEIGH: some row's
+// reference is not the page's v scale (w may not be 1). (Exponents are formed in packed pairs, as the scores
 // lie; what follows 2^x is scalar: packing it again costs more moves than it saves.)
 template <bool MASKED, bool WEIGH>
-__device__ __forceinline__ void row_weights(const uint32_t (&u)[16], uint32_t seen, float2 kv, const RowState& st,
+__device__ __forceinline__ void row_weights(const uint32_t (&u)[16], uint32_t seen, float ks, float w, const RowState& st,
                                             float& most, float& sum, uint32_t (&p)[8]) {
     const uint64_t nm = pk2(kBias - st.m, kBias - st.m);
-    const float f = kv.x * st.c, w = kv.y * st.rv;
+    const float f = ks * st.c;
     const uint64_t f2 = pk2(f, f);
     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -218,30 +229,49 @@ __device__ __forceinline__ void row_weights(const uint32_t (&u)[16], uint32_t se
     sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
-// Raises a row's maximum to that of columns 16 q .. 16 q + 15 of the step (their
-// scores are still in TMEM) and scales the weights and outputs so far; returns
-// the new maximum and the factor.
-__device__ __noinline__ float2 raise_row(uint32_t s, uint32_t o, bool have_o, int q, uint32_t seen, float f0, bool real,
-                                         float m) {
-    float top = -INFINITY;
+// Raises the maximum of the rows that need it to that of columns 16 q .. 63 of
+// step b (their scores are still in TMEM), and the reference to the largest
+// weight x v scale there, and scales those rows' weights and outputs so far;
+// returns the new maximum and reference and the factor of the sum of weights. The
+// reference is a page's v scale itself where the largest weight lies there
+// (weights need no factor then), and at least 2^-126: its reciprocal is finite.
+// Calls are rare, but all warps of a half wait for one: of the step's columns
+// rather than the 16 at hand, and with a wide lag, a third as many are needed.
+__device__ __noinline__ float3 raise_row(uint32_t s, uint32_t o, bool have_o, int q, int b, uint32_t seen0, uint32_t seen1,
+                                         const float2* scale, int page_log, float c, bool need, float m, float vref) {
+    float mn = m, vn = 0.f;
 #pragma unroll 1
-    for (int i = 0; i < 16; i += 8) {
-        float v[8];
-        tmem_ld<8>(s + 16 * q + i, v);
+    for (int i = q; i < 4; ++i) {
+        const uint32_t seen = (i < 2 ? seen0 : seen1) >> (16 * (i & 1));
+        const float2 kv = scale[(64 * b + 16 * i) >> page_log];
+        const float f0 = kv.x * c;
+        float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if ((seen >> (i + k)) & 1u) top = fmaxf(top, v[k] * f0);
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            tmem_ld<8>(s + 16 * i + 8 * h, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if ((seen >> (8 * h + k)) & 1u) top = fmaxf(top, v[k] * f0);
+        }
+        if (need && top > -INFINITY) {  // vn is relative to mn
+            const float up = fmaxf(mn, top);
+            vn = fmaxf(mn == up ? vn : exp2_approx(mn - up) * vn, top == up ? kv.y : exp2_approx(top - up) * kv.y);
+            mn = up;
+        }
     }
-    const float mn = real ? fmaxf(m, top) : 0.f;
-    const float f = m == mn ? 1.f : exp2_approx(m - mn);
-    rescale_row(s, 8 * q, o, have_o, f);
-    return make_float2(mn, f);
+    const float f = m == mn ? 1.f : exp2_approx(m - mn), old = vref * f;
+    vn = need ? fmaxf(fmaxf(old, vn), 0x1p-126f) : vref;
+    const float fo = vn == old ? 1.f : old / vn;
+    if (__any_sync(kFull, fo != 1.f)) rescale_row(s, 8 * q, o, have_o, fo);
+    return make_float3(mn, vn, f);
 }
 
 // The weights of a row over step b of a tile (64 tokens), 16 columns at a time,
 // over the front of its scores: column pair i of P takes the place of score i,
-// which has been read by then. Where a chunk's largest exponent passes the lag,
-// the warp raises its rows' maxima first. (Short loops: 32 columns at a time
+// which has been read by then. Where a row's largest exponent in a chunk passes
+// the lag, or its weights times the v scale may (their sum bounds them), the row's
+// maximum and reference are raised first. (Short loops: 32 columns at a time
 // took 2 % longer, 64 in a row 15 %: eight warps run this code each at a place
 // of its own, and fetching longer code costs more than its overlap gains.)
 template <bool MASKED, bool WEIGH>
@@ -254,19 +284,24 @@ __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, in
         const float2 kv = scale[col >> page_log];
         uint32_t u[16];
         TmemLoad<16>::run(s + 16 * q, u);
-        float most, sum;
+        float most, sum, w = WEIGH ? value_factor(kv.y, st) : 1.f;
         uint32_t p[8];
-        row_weights<MASKED, WEIGH>(u, seen, kv, st, most, sum, p);
-        if (__any_sync(kFull, real && most > kBias + kLag)) {
-            if (have_o) {  // O is quiet once the step before is done
+        row_weights<MASKED, WEIGH>(u, seen, kv.x, w, st, most, sum, p);
+        const bool need = real && (most > kBias + kLag || (WEIGH && w > 1.f && sum * w > kMost));
+        if (__any_sync(kFull, need)) {
+            if (have_o) {  // O is quiet once the step before is done; the one in
+                           // front of that is, it came before these scores
                 wait(pv_done, b ^ 1);
                 tc_fence_after();
             }
-            const float2 r = raise_row(s, o, have_o, q, seen, kv.x * st.c, real, st.m);
+            const float3 r = raise_row(s, o, have_o, q, b, MASKED ? view.bits(64 * b) : kFull,
+                                       MASKED ? view.bits(64 * b + 32) : kFull, scale, page_log, st.c, need, st.m, st.vref);
             st.m = r.x;
-            st.l *= r.y;
+            st.vref = r.y;
+            st.l *= r.z;
             TmemLoad<16>::run(s + 16 * q, u);
-            row_weights<MASKED, WEIGH>(u, seen, kv, st, most, sum, p);
+            if (WEIGH) w = value_factor(kv.y, st);
+            row_weights<MASKED, WEIGH>(u, seen, kv.x, w, st, most, sum, p);
         }
         st.l += sum;
         tmem_st8(s + 8 * q, reinterpret_cast<float*>(p));
@@ -529,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 proxy_fence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready[hf]));
-                RowState st{c, real ? -INFINITY : 0.f, 0.f, 0.f, 0.f};
+                RowState st{c, real ? -INFINITY : 0.f, 0.f, 0.f};
 #pragma unroll 1
                 for (int j = j0; j < j1; ++j, ++it, ++n) {
                     const uint32_t ring = it % kRing;
@@ -548,22 +583,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kFull, lane < slots && ((ok >> lane) & 1u) ? __float_as_uint(scale[lane].y) : 0u));
                     const float vmin = __uint_as_float(__reduce_min_sync(
                         kFull, lane < slots && ((ok >> lane) & 1u) ? __float_as_uint(scale[lane].y) : 0x7f800000u));
-                    const bool plain = whole && vmin >= fmaxf(vmax, st.vref);
+                    const bool one = whole && vmin == vmax;  // one v scale in the tile
 #pragma unroll 1
                     for (int b = 0; b < 2; ++b) {
                         wait(smem_u32(&ms.s_full[hf][b]), n & 1);
                         tc_fence_after();
                         const bool have_o = j > j0 || b > 0;
-                        if (vmax > st.vref) {
-                            if (have_o) {  // O is quiet once the step before is done; the one in
-                                           // front of that is, it came before these scores
-                                wait(pv_done, b ^ 1);
-                                tc_fence_after();
-                                rescale_row(s_at, 0, o_at, true, st.vref / vmax);
-                            }
-                            st.vref = vmax;
-                            st.rv = 1.f / vmax;
-                        }
+                        const bool plain = one && __all_sync(kFull, !real || vmax == st.vref);
                         if (plain) row_step<false, false>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
                         else if (whole) row_step<false, true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
                         else row_step<true, true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
@@ -576,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const bool complete = walk.complete();
                 float* part = a.part + (2 * blockIdx.x + (walk.first ? 0 : 1)) * part_stride<RC>();
-                const float inv = complete ? (st.l == 0.f ? 0.f : st.vref / st.l) : st.vref;
+                const float inv = complete ? (st.l == 0.f ? 0.f : 1.f / st.l) : 1.f;
                 __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + out_row * kD;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
@@ -584,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld<32>(o_at + 32 * q, v);
                     const uint32_t nan = ms.nan[r][q];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = (nan >> i) & 1u ? NAN : v[i] * inv;
+                    for (int i = 0; i < 32; ++i) v[i] = (nan >> i) & 1u ? NAN : v[i] * inv * st.vref;
                     if (!real) continue;
                     if (complete) {
 #pragma unroll

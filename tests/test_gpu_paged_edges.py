@@ -1,0 +1,105 @@
+"""The paged 8-bit cache at the edges of what its calls allow, on the GPU: value
+scales that lie far apart, rows and tokens that others do not see, queries with
+one large channel, lengths and rows out of range, a caller's own scales, calls
+in either order."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attention_decode_b200 as nsnq
+from oracle import paged as OP
+from test_gpu_paged import Batch, D
+
+pytestmark = pytest.mark.gpu
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def bounded(got, q, b, codes, scales, window=0, sinks=0, scale=1 / math.sqrt(D)):
+    """Attention against fp64 with a bound that holds whatever the value scales
+    are. Each weight is off by a relative e, as for test_gpu_paged.check_out: an
+    output by 2 e sum p |v| / sum p. A term (weight times its page's value scale)
+    is held in steps of 2^-23 of the row's largest such term, or finer, so half a
+    step of it is lost at most, for each token, times a code of at most 448. Then
+    half a step of the output type."""
+    table, lens, cu = b.table.tolist(), b.lens, b.cu
+    for s, length in enumerate(lens):
+        for r in range(cu[s], cu[s + 1]):
+            pos = length - (cu[s + 1] - r)
+            seen = [t for t in range(pos + 1) if not window or t > pos - window or t < sinks]
+            if not seen:
+                assert (got[r] == 0).all()
+                continue
+            ids, at = np.array([table[s][t // b.page] for t in seen]), np.array([t % b.page for t in seen])
+            for h in range(b.hq):
+                g = h // (b.hq // b.hkv)
+                kk = OP.VALUES[codes[0][ids, g, at]] * scales[0][ids, g].astype(np.float64)[:, None]
+                vs = scales[1][ids, g].astype(np.float64)
+                vv = OP.VALUES[codes[1][ids, g, at]] * vs[:, None]
+                x = q[r, h].double().cpu().numpy()
+                p = np.exp(kk @ x * scale - (kk @ x * scale).max())
+                want, size = p @ vv / p.sum(), p @ np.abs(vv) / p.sum()
+                reach = (np.abs(kk) @ np.abs(x)).max() * abs(scale)
+                e = 2.0 ** -18 + 160 * 2.0 ** -23 * reach + (2.0 ** -11 if got.dtype == torch.bfloat16 else 0.0)
+                lost = len(seen) * 2.0 ** -24 * 448.0 * (p * vs).max() / p.sum()
+                tol = torch.finfo(got.dtype).eps / 2 * np.abs(want) + 2 * e * size + lost
+                err = np.abs(got[r, h].double().cpu().numpy() - want)
+                assert (err <= tol).all(), (r, h, (err / np.maximum(tol, 1e-300)).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 4, 2), (4, 4, 2), (16, 2, 2), (90, 4, 2), (40, 8, 2)])
+def test_value_scales_far_apart(rows, hq, hkv, dtype):
+    """Rows that see pages of tiny values only, rows behind them that see huge ones too, in either order."""
+    for sign, seed in ((1, 1), (-1, 2), (0, 3)):
+        b = Batch([rows, rows], [0, 60], hq, hkv, 16, dtype, seed=seed)
+        slot = torch.arange(b.cols)[None, :, None].expand(2, b.cols, hkv)
+        e = sign * (7 * slot - 30) if sign else torch.randint(-60, 30, slot.shape, generator=torch.Generator().manual_seed(rows))
+        b.scales[1][b.table.long()] = torch.exp2(e.float())
+        pc, (table, lens, cu) = b.cache(), b.dev()
+        got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=rows, out_dtype=dtype)
+        bounded(got, b.q, b, *b.stored())
+
+
+@pytest.mark.parametrize("rows", [1, 4, 60])
+@pytest.mark.parametrize("small,large", [(-20, 10), (-60, 40), (-126, 0)])
+def test_weight_on_a_page_of_small_values(rows, small, large):
+    """Nearly all the weight on a token whose page holds far smaller values than the others' pages."""
+    b = Batch([rows], [300], 4, 2, 16, seed=rows)
+    b.q = b.q.abs() + 1
+    b.scales[0].fill_(2.0 ** -9)
+    b.scales[1].fill_(2.0 ** large)
+    page = b.table[0, 5].long()
+    b.codes[0][page, :, 3] = 0x7E                  # 448 / 512 in every channel
+    b.scales[1][page] = 2.0 ** small
+    b.scales[0][page] = 2.0 ** -9
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=rows, softmax_scale=1.0)
+    bounded(got, b.q, b, *b.stored(), scale=1.0)
+
+
+@pytest.mark.parametrize("rows,hq,page,window,sinks", [(8, 4, 16, 0, 0), (3, 2, 16, 30, 2), (40, 4, 16, 0, 0),
+                                                       (300, 2, 16, 0, 0), (200, 4, 32, 50, 3), (128, 2, 64, 0, 0)])
+def test_unseen_tokens_change_no_bit(rows, hq, page, window, sinks):
+    """Other keys, values and scales behind a row's position: the same bits, in both kernels."""
+    before = page - 4
+    b = Batch([rows], [before], hq, 2, page, seed=rows)
+    for s in b.scales:
+        s.copy_(torch.exp2(torch.randint(-9, -4, s.shape, generator=torch.Generator().manual_seed(rows)).float()))
+    q, (table, lens, cu) = b.q.cuda(), b.dev()
+    want = nsnq.nsnq_paged_attn(q, b.cache(), table, lens, cu, max_rows=rows, window=window, sinks=sinks)
+    g = torch.Generator().manual_seed(rows + 1)
+    for border in range(1, b.cols):                # pages from this one on are others
+        for trial in range(3):
+            pc, ids = b.cache(), b.table[0, border:].long().cuda()
+            for c in (pc.k, pc.v):
+                other = torch.randint(0, 256, (len(ids), *c.shape[1:]), generator=g).to(torch.uint8)
+                c.view(torch.uint8)[ids] = other.cuda()
+            for s, (lo, hi) in ((pc.k_scales, ((-9, 5), (-9, 0), (20, 60))[trial]), (pc.v_scales, ((20, 60), (-60, 60), (-9, 3))[trial])):
+                s[ids] = torch.exp2(torch.randint(lo, hi, (len(ids), 2), generator=g).float()).cuda()
+            got = nsnq.nsnq_paged_attn(q, pc, table, lens, cu, max_rows=rows, window=window, sinks=sinks)
+            n = border * page - before
+            assert torch.equal(got[:n], want[:n]), (border, trial)
