@@ -25,9 +25,19 @@ nsnq_status set_error(nsnq_status s, const char* fmt, ...);
 // Multiprocessor count of the current device, queried once per device.
 int device_sm_count();
 
+// A launch's dynamic shared memory, and the most that any launch of its kernel
+// takes where that is not always the same.
+struct Smem {
+    size_t bytes, most;
+    Smem(size_t b) : bytes(b), most(b) {}
+    Smem(size_t b, size_t m) : bytes(b), most(m) {}
+};
+
 // The dynamic shared-memory limit of one kernel, set once per device (one
-// bit per device in `ready`). A device reset drops the attribute; a launch
-// that then fails with cudaErrorInvalidValue is retried once by launch_smem.
+// bit per device in `ready`), for every launch of it. A device reset drops the
+// attribute; a launch that then fails with cudaErrorInvalidValue is retried once
+// by launch_smem. No failure is left behind as the runtime's last error: the next
+// call would report it as its own.
 template <typename K>
 cudaError_t ensure_smem(K kern, int bytes, std::atomic<unsigned long long>& ready, bool force) {
     int dev = 0;
@@ -37,22 +47,23 @@ cudaError_t ensure_smem(K kern, int bytes, std::atomic<unsigned long long>& read
     if (!force && bit && (ready.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && bit) ready.fetch_or(bit, std::memory_order_relaxed);
+    if (e != cudaSuccess) (void)cudaGetLastError();
     return e;
 }
 
-// Launch kern<<<grid, block, smem, s>>>(args...) with its shared-memory limit
+// Launch kern<<<grid, block, smem.bytes, s>>>(args...) with its shared-memory limit
 // set (once per device).
 template <typename... P, typename... A>
 cudaError_t launch_smem(void (*kern)(P...), std::atomic<unsigned long long>& ready, dim3 grid,
-                        dim3 block, size_t smem, cudaStream_t s, A&&... args) {
-    cudaError_t e = ensure_smem(kern, (int)smem, ready, false);
+                        dim3 block, Smem smem, cudaStream_t s, A&&... args) {
+    cudaError_t e = ensure_smem(kern, (int)smem.most, ready, false);
     if (e != cudaSuccess) return e;
-    kern<<<grid, block, smem, s>>>(args...);
+    kern<<<grid, block, smem.bytes, s>>>(args...);
     e = cudaGetLastError();
     if (e == cudaErrorInvalidValue) {  // attribute lost (device reset): set it again, once
-        e = ensure_smem(kern, (int)smem, ready, true);
+        e = ensure_smem(kern, (int)smem.most, ready, true);
         if (e != cudaSuccess) return e;
-        kern<<<grid, block, smem, s>>>(args...);
+        kern<<<grid, block, smem.bytes, s>>>(args...);
         e = cudaGetLastError();
     }
     return e;
@@ -63,13 +74,13 @@ cudaError_t launch_smem(void (*kern)(P...), std::atomic<unsigned long long>& rea
 // griddepcontrol.wait before it reads what that kernel wrote.
 template <typename... P, typename... A>
 cudaError_t launch_smem_pdl(void (*kern)(P...), std::atomic<unsigned long long>& ready, dim3 grid,
-                            dim3 block, size_t smem, cudaStream_t s, A&&... args) {
-    cudaError_t e = ensure_smem(kern, (int)smem, ready, false);
+                            dim3 block, Smem smem, cudaStream_t s, A&&... args) {
+    cudaError_t e = ensure_smem(kern, (int)smem.most, ready, false);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = smem.bytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -78,10 +89,12 @@ cudaError_t launch_smem_pdl(void (*kern)(P...), std::atomic<unsigned long long>&
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, args...);
     if (e == cudaErrorInvalidValue) {  // attribute lost (device reset): set it again, once
-        e = ensure_smem(kern, (int)smem, ready, true);
+        (void)cudaGetLastError();
+        e = ensure_smem(kern, (int)smem.most, ready, true);
         if (e != cudaSuccess) return e;
         e = cudaLaunchKernelEx(&cfg, kern, args...);
     }
+    if (e != cudaSuccess) (void)cudaGetLastError();
     return e;
 }
 

@@ -522,8 +522,9 @@ cudaError_t launch_few(const PagedAppendArgs& a, cudaStream_t s) {
 template <typename XT, int PAGE>
 cudaError_t launch_page(const PagedAppendArgs& a, int64_t grid, cudaStream_t s) {
     static std::atomic<unsigned long long> ready{0};
+    constexpr size_t ring = app_ahead<XT>() * PAGE * kD * sizeof(XT), turns = PAGE * 64 * sizeof(float2);
     return launch_smem_pdl(paged_append_kernel<XT, PAGE>, ready, dim3((unsigned)grid), dim3(AppShape<PAGE>::kThreads),
-                           (a.rope ? PAGE * 64 * sizeof(float2) : 0) + app_ahead<XT>() * PAGE * kD * sizeof(XT), s, a);
+                           Smem(ring + (a.rope ? turns : 0), ring + turns), s, a);
 }
 template <typename XT>
 cudaError_t launch_type(const PagedAppendArgs& a, int64_t grid, cudaStream_t s) {

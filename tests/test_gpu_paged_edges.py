@@ -3,6 +3,9 @@ scales that lie far apart, rows and tokens that others do not see, queries with
 one large channel, lengths and rows out of range, a caller's own scales, calls
 in either order."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -13,6 +16,7 @@ from oracle import paged as OP
 from test_gpu_paged import Batch, D
 
 pytestmark = pytest.mark.gpu
+
 
 def i32(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
@@ -103,3 +107,36 @@ def test_unseen_tokens_change_no_bit(rows, hq, page, window, sinks):
             got = nsnq.nsnq_paged_attn(q, pc, table, lens, cu, max_rows=rows, window=window, sinks=sinks)
             n = border * page - before
             assert torch.equal(got[:n], want[:n]), (border, trial)
+
+
+ORDERS = """
+import torch
+import attention_decode_b200 as nsnq
+dev = dict(device="cuda", dtype=torch.%(dtype)s)
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+pc = nsnq.PagedCache.empty(4, 2, %(page)d)
+k, v = torch.ones(9, 2, 128, **dev), torch.ones(9, 2, 128, **dev)
+args = (pc, i32([[0, 1]]), i32([9]), i32([0, 9]))
+graph = torch.cuda.CUDAGraph()
+nsnq.nsnq_paged_append(k, v, *args, rope_base=%(first)s)
+with torch.cuda.graph(graph):
+    nsnq.nsnq_paged_append(k, v, *args, rope_base=%(second)s)
+graph.replay()
+cb = nsnq.Codebook(torch.randn(256, 8, device="cuda"))
+cache = nsnq.Cache.empty(1, 1, 64, 8)
+nsnq.nsnq_encode(torch.randn(1, 1, 64, 128, device="cuda"), cb, cache)
+torch.cuda.synchronize()
+assert cache.codes.any()
+print("both orders fine")
+"""
+
+
+@pytest.mark.parametrize("page,dtype", [(16, "bfloat16"), (64, "bfloat16"), (64, "float32"), (128, "float32")])
+@pytest.mark.parametrize("first,second", [("0.0", "10000.0"), ("10000.0", "0.0")])
+def test_appends_with_and_without_rotation_in_either_order(first, second, page, dtype):
+    """In a process of its own: what the first call sets up for a kernel is enough for the second, captured one,
+    and no error is left for the next call of the library."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ORDERS % dict(first=first, second=second, page=page, dtype=dtype)
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "both orders fine" in run.stdout, run.stderr[-2000:]
