@@ -78,8 +78,9 @@ __device__ __forceinline__ void paged_report(const PagedSeqs& s, uint32_t bits) 
 }
 
 // Sequence b: its first row, its row count and its tokens with those rows.
-// Rows are clamped into [0, n_rows]; a length that the table row cannot hold
-// makes the sequence empty of tokens (len = 0).
+// A length that the table row cannot hold, or rows outside [0, n_rows] (clamped
+// into it), make the sequence empty of tokens (len = 0): where its tokens are is
+// not known, and nothing of it is stored or attended.
 struct PagedSeq {
     int row0, rows, len;
     uint32_t bad;
@@ -97,7 +98,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedSeqs& s, int b) {
     r.rows = (int)(chi - clo);
     r.len = s.seq_lens[b];
     r.bad = (clo != lo || chi != hi) ? kBadLength : 0u;
-    if (r.len < 0 || r.len > s.capacity) {
+    if (r.bad || r.len < 0 || r.len > s.capacity) {
         r.len = 0;
         r.bad = kBadLength;
     }

@@ -419,8 +419,12 @@ typedef struct {
 typedef enum {
     NSNQ_PAGED_BAD_PAGE = 1,   /* a needed page_table entry outside [0, num_pages): its tokens
                                   were left out (not stored; not seen by attention) */
-    NSNQ_PAGED_BAD_LENGTH = 2, /* a sequence longer than its table row, with more rows than tokens
-                                  or than max_rows, or rows outside [0, n_rows): left out */
+    NSNQ_PAGED_BAD_LENGTH = 2, /* a sequence longer than its table row, or with rows outside
+                                  [0, n_rows): all of it left out (attention gives zeros for the
+                                  rows that there are). More rows than tokens: not stored; attention
+                                  gives zeros for the rows in front of the first token. More rows
+                                  than max_rows: those past it are left out, their outputs not
+                                  written */
     NSNQ_PAGED_TIMEOUT = 4     /* a wait inside the attention kernel passed its limit: the outputs
                                   of that call are void */
 } nsnq_paged_status;

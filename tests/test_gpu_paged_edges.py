@@ -13,7 +13,7 @@ import torch
 
 import attention_decode_b200 as nsnq
 from oracle import paged as OP
-from test_gpu_paged import Batch, D
+from test_gpu_paged import Batch, D, check_pool
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +140,36 @@ def test_appends_with_and_without_rotation_in_either_order(first, second, page, 
     code = ORDERS % dict(first=first, second=second, page=page, dtype=dtype)
     run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and "both orders fine" in run.stdout, run.stderr[-2000:]
+
+
+@pytest.mark.parametrize("cu,lens", [([0, 10], [20]), ([-2, 6], [20]), ([0, 3, 12], [9, 30]), ([0, 5, 3, 8], [9, 9, 9]),
+                                     ([0, 1000000], [20]), ([0, 2, 40, 42], [7, 60, 8]), ([0, 2, 4, 6, 7, 20], [9, 20, 33, 17, 50])])
+def test_rows_out_of_range_are_left_out(cu, lens):
+    """A sequence whose rows the row tensors do not hold: nothing stored, nothing attended."""
+    B, n = len(lens), 8
+    b = Batch([n] * B, [40] * B, 4, 2, 16, seed=B)
+    pc, table = b.cache(), b.table.cuda()
+    q, k, v = (x[:n].cuda() for x in (b.q, b.k, b.v))
+    good = [s for s in range(B) if 0 <= cu[s] <= cu[s + 1] <= n]
+    bad = [s for s in range(B) if s not in good]
+    nsnq.nsnq_paged_append(k, v, pc, table, i32(lens), i32(cu), q=q, rope_base=b.base)
+    assert int(pc.status) == nsnq.PAGED_BAD_LENGTH
+    codes, scales = b.stored()
+    for s in good:
+        if cu != [0, 5, 3, 8]:                     # (overlapping rows: each sequence stores its own)
+            OP.append(k.double().cpu().numpy(), v.double().cpu().numpy(), codes, scales, [b.table[s].tolist()], [lens[s]],
+                      cu[s:s + 2], b.base)
+    if cu != [0, 5, 3, 8]:
+        check_pool(pc, codes, scales)
+    pc = b.cache()
+    got = nsnq.nsnq_paged_attn(q, pc, table, i32(lens), i32(cu), max_rows=100)
+    assert int(pc.status) == nsnq.PAGED_BAD_LENGTH
+    for s in bad:
+        lo, hi = max(0, min(n, cu[s])), max(0, min(n, cu[s + 1]))
+        if cu != [0, 5, 3, 8]:
+            assert (got[lo:hi] == 0).all()
+    for s in good:
+        if cu != [0, 5, 3, 8]:
+            alone = nsnq.nsnq_paged_attn(q[cu[s]:cu[s + 1]], pc, table[s:s + 1], i32(lens[s:s + 1]),
+                                         i32([0, cu[s + 1] - cu[s]]), max_rows=100)
+            assert (got[cu[s]:cu[s + 1]].float() - alone.float()).abs().max() <= 0.02 * alone.float().abs().max()
