@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     for (int k = lane; k < n; k += 32) {
         const float* p = part(k) + RC * kD + r;
         const float m = p[0], l = p[RC];
-        const float f = l != 0.f ? exp2_approx(m - top) : 0.f;
+        const float f = l != 0.f ? exp2_approx(m - top) : -1.f;  // -1: the row sees nothing of the part
         if (k % kShare == w0) factor[warp][k / kShare] = f;
         if (l != 0.f) sum = fmaf(f, l, sum);
     }
@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         const float f = factor[warp][k / kShare];
         const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (f != 0.f) acc[i] = fmaf(f, w[i], acc[i]);
+        for (int i = 0; i < 4; ++i)  // a factor of 0 keeps the part's NaN, and nothing else of it
+            if (f != -1.f && (f != 0.f || isnan(w[i]))) acc[i] = fmaf(f, w[i], acc[i]);
     }
     if (kShare > 1) {
         sums[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);

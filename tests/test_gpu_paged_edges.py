@@ -173,3 +173,20 @@ def test_rows_out_of_range_are_left_out(cu, lens):
             alone = nsnq.nsnq_paged_attn(q[cu[s]:cu[s + 1]], pc, table[s:s + 1], i32(lens[s:s + 1]),
                                          i32([0, cu[s + 1] - cu[s]]), max_rows=100)
             assert (got[cu[s]:cu[s + 1]].float() - alone.float()).abs().max() <= 0.02 * alone.float().abs().max()
+
+
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_nan_value_under_a_vanishing_weight(rows):
+    """A NaN value counts wherever its row sees it, also where its weight is too small for fp32 in another
+    CTA's part of the row."""
+    b = Batch([rows], [20000 - rows], 4, 2, 128, seed=rows)
+    b.q = b.q.abs() + 1
+    b.codes[0][:] = 0
+    b.codes[0][b.table[0, -1].long(), :, 31 - rows] = 0x7E     # a seen token of a large score
+    b.codes[1][b.table[0, 0].long(), 1, 5, 77] = 0x7F
+    b.scales[0].fill_(1.0)
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    got = torch.isnan(nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=rows)).cpu()
+    want = torch.zeros(rows, 4, D, dtype=torch.bool)
+    want[:, 2:, 77] = True
+    assert torch.equal(got, want)
