@@ -16,7 +16,7 @@
 //   O[channel][piece, row] += V^T w   (M = 128 channels, K = 128 tokens).
 // Two pieces hold a bf16 query exactly (8 bits; the row scaled to at most
 // 256, elements below 2^-14 of that lose bits to an absolute 2^-24 of it);
-// three hold weights to 2^-12, six hold fp32 queries and weights to 2^-24.
+// three hold weights to 2^-10, six hold fp32 queries and weights to 2^-24.
 // Products of codes are exact in fp32, and fp32 is what TMEM accumulates.
 // (The alternative, widening K and V to 16 bits for kind::f16, would write and
 // read every tile once more through shared memory: 64 KB more for the 32 KB
@@ -51,7 +51,11 @@ namespace {
 
 constexpr int kThreads = 192;  // warps 0-3: tokens / channels; 4: TMA; 5: MMA issue
 constexpr float kLag = 5.f, kBias = 2.f;  // weights stay below 2^7 (1 + 2^-20)
-constexpr int kShift = 6;                  // bits between the pieces of a weight
+// Bits between the pieces of a weight. A piece rounds its value to within 2^(k - 4)
+// below 2^(k + 1), so that with 5 the next piece stays below the same bound. With 6
+// it doubles: of a weight from 2^6 to 2^7 the third piece may be held at 448 where it
+// would be 512, 2^-12 of the weight besides fp16's 2^-11.
+constexpr int shift_of(int pieces) { return pieces <= 3 ? 6 : 5; }
 constexpr int kMaxSlots = 8;   // pages per tile (page_size 16)
 constexpr int kMaxRows = 16;   // of a unit
 // Tiles that a unit's queries and epilogue cost (1, 2, 3: 13 x 4 rows 57.0, 55.3,
@@ -100,7 +104,7 @@ __device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
     return r;
 }
-__device__ __forceinline__ uint32_t f16x2_rest(uint32_t h, uint32_t c) {  // (h - c) * 2^kShift, exact
+__device__ __forceinline__ uint32_t f16x2_rest(uint32_t h, uint32_t c) {  // (h - c) * 2^6, exact
     uint32_t r;
     asm("{.reg .b32 d;\n\tsub.f16x2 d, %1, %2;\n\tmul.f16x2 %0, d, %3;}" : "=r"(r) : "r"(h), "r"(c), "r"(0x54005400u));
     return r;
@@ -121,8 +125,8 @@ __device__ __forceinline__ void weight_pieces(float w0, float w1, uint32_t (&out
         for (int k = 0; k < PP; ++k) {
             out[k] = e4m3x2(w0, w1);
             const uint32_t h = e4m3x2_to_f16x2(out[k]);
-            w0 = (w0 - f16_lo(h)) * (float)(1 << kShift);
-            w1 = (w1 - f16_hi(h)) * (float)(1 << kShift);
+            w0 = (w0 - f16_lo(h)) * (float)(1 << shift_of(PP));
+            w1 = (w1 - f16_hi(h)) * (float)(1 << shift_of(PP));
         }
     }
 }
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int k = (c0 + i) / RC, r = (c0 + i) % RC;
-                    if (k < PP) o[r] = k == 0 ? v[i] : fmaf(v[i], 1.f / (float)(1ull << (kShift * k)), o[r]);
+                    if (k < PP) o[r] = k == 0 ? v[i] : fmaf(v[i], 1.f / (float)(1ull << (shift_of(PP) * k)), o[r]);
                 }
             }
             tc_fence_before();

@@ -490,8 +490,8 @@ size_t nsnq_paged_attn_workspace(int64_t n_rows, int B, int Hq, int Hkv, int D, 
  * and the limits are those of nsnq_paged_append; every value of the cache's
  * scales must be finite and positive (powers of two or not).
  * Scores and sums are fp32. With bf16 q and out, a weight times its page's v
- * scale is rounded to 11 bits or to steps of 2^-23 of the row's largest such
- * product, whichever is coarser (the products, not the weights alone: a
+ * scale is off by at most 2^-10 of itself or by half a step of 2^-23 of the
+ * row's largest such product, whichever is more (the products, not the weights alone: a
  * token's share counts, not what scale its page has, nor the scales of pages
  * that the row does not see); with fp32 q or out, queries and weights keep 24
  * bits, at a several times lower rate for prompts. The same call gives the

@@ -190,3 +190,33 @@ def test_nan_value_under_a_vanishing_weight(rows):
     want = torch.zeros(rows, 4, D, dtype=torch.bool)
     want[:, 2:, 77] = True
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("hq,q_dtype,out_dtype", [(64, torch.float32, torch.float32), (32, torch.float32, torch.float32),
+                                                  (64, torch.bfloat16, torch.float32), (32, torch.float32, torch.bfloat16)])
+def test_fp32_weights_above_a_lagging_maximum(hq, q_dtype, out_dtype):
+    """One token of the second tile takes nearly all the weight while the row's maximum lags behind it by 4 to 5
+    bits: it keeps its 24 bits. Scores are one product each: off by 2^-21 of at most 4 (their scale's rounding, the
+    product's and the exponent's), 2^-18 for exp2 and the sums, twice for the quotient. The other 200 tokens' weights
+    are 2^-36 of the largest and less: what the six pieces, 4 bits and then 5 each from 2^2 or more down to 2^-34,
+    hold of them is off by half that step each, 2^-37 of the largest, times a code of at most 448."""
+    n = 24
+    b = Batch([1] * n, [201] * n, hq, 8, 64, torch.float32, seed=hq)
+    g = torch.Generator().manual_seed(hq)
+    b.codes[0].zero_()
+    b.scales[0].fill_(1.0)
+    b.scales[1].fill_(1.0)
+    for t, code in ((3, 0x00), (200, 0x38)):       # k . q = 0 and q_0; elsewhere -8 q_0
+        for s in range(n):
+            if t == 3:
+                b.codes[0][b.table[s].long(), :, :, 0] = 0xD0
+            b.codes[0][b.table[s, t // 64].long(), :, t % 64, 0] = code
+    b.q.zero_()
+    b.q[:, :, 0] = ((4.0 + torch.rand(n, hq, generator=g)) * math.log(2.0)).to(q_dtype).float()
+    pc, (table, lens, _) = b.cache(), b.dev()
+    got = nsnq.nsnq_paged_attn(b.q.to(q_dtype).cuda(), pc, table, lens, softmax_scale=1.0, out_dtype=out_dtype).double().cpu().numpy()
+    codes, scales = b.stored()
+    want, weight, _, _ = OP.attention(b.q.double().numpy(), codes, scales, b.table.tolist(), b.lens, list(range(n + 1)), 0, 0, 1.0)
+    tol = 2 * (2.0 ** -18 + 4 * 2.0 ** -21) * weight + 200 * 2.0 ** -37 * 448 + torch.finfo(out_dtype).eps / 2 * np.abs(want)
+    err = np.abs(got - want)
+    assert (err <= tol).all(), ((err > tol).sum(), (err / np.maximum(tol, 1e-300)).max())
