@@ -5,8 +5,11 @@
 // fastest, in two halves of 128 rows; a row is a TMEM lane and one thread's.
 // Per tile of 128 tokens and half:
 //   S = Q K^T      tcgen05.mma kind::f8f6f4: K as the cache holds it, Q as two
-//                  e4m3 pieces of 4 significant bits in one accumulator (a bf16
-//                  query scaled to at most 448 is their sum, up to 2^-10),
+//                  pieces in one accumulator: an e4m3 one of 4 significant bits,
+//                  and what it leaves in e5m2 (of the 8 bits of a bf16 query the
+//                  4 below have 3 significant ones, and e5m2 reaches down to
+//                  2^-16). With a row scaled to at most 448, that is an element
+//                  down to 2^-6 exactly, and a smaller one up to 2^-14,
 //   p = 2^(s - m)  one thread per row: no value crosses a thread,
 //   O += P V       kind::f16, P from TMEM (over S), V widened to fp16 (exact)
 //                  in shared memory by a warpgroup of its own.
@@ -74,7 +77,14 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
     return r;
 }
 
-// Queries of the warp's 32 rows (from unit row `first` on) as two e4m3 pieces,
+// Two e5m2 codes (nearest, ties to even, held at the largest value); the low byte holds a.
+__device__ __forceinline__ uint32_t e5m2x2(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Queries of the warp's 32 rows (from unit row `first` on) as two pieces,
 // eight lanes to a row, 16 channels each; returns the scale of this lane's row.
 __device__ __forceinline__ float write_rows(const PagedAttnArgs& a, const PagedUnit& u, int h, int first, uint8_t* hi,
                                             int lrow0) {
@@ -131,8 +141,8 @@ __device__ __forceinline__ float write_rows(const PagedAttnArgs& a, const PagedU
             const uint32_t c0 = e4m3x2(y[0], y[1]), c1 = e4m3x2(y[2], y[3]);
             const uint32_t h0 = e4m3x2_to_f16x2(c0), h1 = e4m3x2_to_f16x2(c1);
             p[k] = bad ? 0x7f7f7f7fu : (c0 | (c1 << 16));
-            l[k] = bad ? 0u : (e4m3x2(y[0] - f16_lo(h0), y[1] - f16_hi(h0)) |
-                               (e4m3x2(y[2] - f16_lo(h1), y[3] - f16_hi(h1)) << 16));
+            l[k] = bad ? 0u : (e5m2x2(y[0] - f16_lo(h0), y[1] - f16_hi(h0)) |
+                               (e5m2x2(y[2] - f16_lo(h1), y[3] - f16_hi(h1)) << 16));
         }
         const int lrow = lrow0 + 4 * i + (lane >> 3), at = lrow * 128 + ((c ^ (lrow & 7)) << 4);
         *reinterpret_cast<uint4*>(hi + at) = make_uint4(p[0], p[1], p[2], p[3]);
@@ -424,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A step is 64 tokens: half of a tile. The scores of step i + 2 take the
             // place of the weights of step i, behind their P V (MMAs of a CTA run in
             // the order of issue), so that a half always has its next scores ready.
-            constexpr uint32_t id_s = mma_idesc(128, 64, false, false), id_o = mma_idesc(128, 128, false, true);
+            constexpr uint32_t id_s = mma_idesc(128, 64, false, false), id_lo = id_s | kA_e5m2, id_o = mma_idesc(128, 128, false, true);
             uint32_t seg[2] = {0, 0}, np[2] = {0, 0};  // segments and weight steps of each half
 #pragma unroll 1
             for (; walk.live(); walk.next()) {
@@ -461,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint64_t qa = desc_sw128(sb + kQ + hf * 32768u, 16, 1024);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)  // 32 channels each; the pieces one after the other
-                                mma_f8(tmem + hf * 128 + b * 64, qa + (k >> 2) * 1024 + 2 * (k & 3), kb + 2 * (k & 3), id_s,
-                                       k > 0);
+                                mma_f8(tmem + hf * 128 + b * 64, qa + (k >> 2) * 1024 + 2 * (k & 3), kb + 2 * (k & 3),
+                                       k < 4 ? id_s : id_lo, k > 0);
                             mma_commit(smem_u32(&ms.s_full[hf][b]));
                         }
                     }

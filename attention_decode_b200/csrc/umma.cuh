@@ -208,7 +208,9 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint
     return desc_plain(addr, lbo, sbo) | (2ull << 61);
 }
 // Instruction descriptor: fp32 accumulator, operand formats as given (f8f6f4:
-// 0 = e4m3; f16: 0 = fp16), M x N, operands K-major unless marked.
+// 0 = e4m3, 1 = e5m2, A's and B's each their own; f16: 0 = fp16), M x N, operands
+// K-major unless marked.
+constexpr uint32_t kA_e5m2 = 1u << 7;
 __host__ __device__ constexpr uint32_t mma_idesc(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
     return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }

@@ -220,3 +220,21 @@ def test_fp32_weights_above_a_lagging_maximum(hq, q_dtype, out_dtype):
     tol = 2 * (2.0 ** -18 + 4 * 2.0 ** -21) * weight + 200 * 2.0 ** -37 * 448 + torch.finfo(out_dtype).eps / 2 * np.abs(want)
     err = np.abs(got - want)
     assert (err <= tol).all(), ((err > tol).sum(), (err / np.maximum(tol, 1e-300)).max())
+
+
+@pytest.mark.parametrize("rows,dtype", [(1, torch.bfloat16), (3, torch.bfloat16), (50, torch.bfloat16), (50, torch.float32)])
+@pytest.mark.parametrize("ratio", [2.0 ** 8, 2.0 ** 12])
+def test_queries_with_one_large_channel(rows, dtype, ratio):
+    """One query channel far above the others, where the keys are zero: the other channels make the scores. Their
+    elements are within 2^13 of the largest, where a bf16 query is held exactly: no term for it in the bound."""
+    b = Batch([rows], [200], 4, 2, 32, dtype, seed=rows)
+    g = torch.Generator().manual_seed(rows)
+    small = (1 + torch.rand(b.q.shape, generator=g)) * torch.where(torch.rand(b.q.shape, generator=g) < 0.5, -1.0, 1.0)
+    b.q = (small / ratio).to(dtype)
+    b.q[:, :, 64] = 1.9
+    b.codes[0][..., 64] = 0
+    b.scales[0].fill_(2.0 ** -8)
+    scale = float(np.float32(0.5 * ratio))
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=rows, softmax_scale=scale, out_dtype=dtype)
+    bounded(got, b.q, b, *b.stored(), scale=scale)
