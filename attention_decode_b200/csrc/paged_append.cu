@@ -326,6 +326,8 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
         const float tiny = 0x1p-148f * inv;  // what rounding among fp32's subnormal values adds
         // a scale that is no power of two (a caller's own) has a rounded inverse
         const bool unsure = rope || (double)inv != inv_d || (__float_as_uint((float)s_new) & 0x7fffffu) != 0;
+        // and a subnormal one (a caller's own) none that fp32 can hold: every code is divided in fp64
+        const uint32_t all = s_new < 0x1p-126 ? 0xffffu : 0u;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
             const int r = rg + p * (kThreads / 8);
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
                 }
                 continue;
             }
-            uint32_t w[4] = {0, 0, 0, 0}, odd = 0;  // odd: channels (16 of them) whose code is not sure
+            uint32_t w[4] = {0, 0, 0, 0}, odd = all;  // odd: channels (16 of them) whose code is not sure
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 const float u0 = lo[p][i] * inv, u1 = lo[p][i + 1] * inv, v0 = hi[p][i] * inv, v1 = hi[p][i + 1] * inv;

@@ -492,11 +492,12 @@ size_t nsnq_paged_attn_workspace(int64_t n_rows, int B, int Hq, int Hkv, int D, 
  * Scores and sums are fp32. A bf16 query's channels are exact down to 2^-13 of
  * the row's largest, smaller ones to within 2^-21 of the largest. With bf16 q
  * and out, a weight times its page's v scale is off by at most 2^-10 of itself
- * or by half a step of 2^-23 of the row's largest such product, whichever is
- * more (the products, not the weights alone: a token's share counts, not what
- * scale its page has, nor the scales of pages that the row does not see); with
- * fp32 q or out, queries and weights keep 24 bits, at a several times lower
- * rate for prompts. The same call gives the same bits every time.
+ * or by half a step of 2^-23 of the row's largest such product (of 2^-118, if
+ * that is larger), whichever is more (the products, not the weights alone: a
+ * token's share counts, not what scale its page has, nor the scales of pages
+ * that the row does not see); with fp32 q or out, queries and weights keep 24
+ * bits, at a several times lower rate for prompts. The same call gives the
+ * same bits every time.
  */
 nsnq_status nsnq_paged_attn(const void* q, nsnq_dtype q_dtype, int64_t n_rows, int64_t q_stride_t,
                             int64_t q_stride_h, const int32_t* cu_rows, int64_t max_rows,

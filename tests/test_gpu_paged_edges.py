@@ -238,3 +238,36 @@ def test_queries_with_one_large_channel(rows, dtype, ratio):
     pc, (table, lens, cu) = b.cache(), b.dev()
     got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=rows, softmax_scale=scale, out_dtype=dtype)
     bounded(got, b.q, b, *b.stored(), scale=scale)
+
+
+@pytest.mark.parametrize("rows,page", [(1, 16), (2, 64), (9, 16), (40, 64)])
+@pytest.mark.parametrize("scale", [1e-40, 2.0 ** -128, 2.0 ** -149, 3e38])
+def test_append_under_extreme_scales_of_a_caller(rows, page, scale):
+    """A page whose own scale is subnormal, or nearly the largest: zeros, tiny values and values that outgrow it."""
+    for grow in (0.0, 1e-40, 1.0):
+        b = Batch([rows, rows], [9, 3], 4, 2, page, torch.float32, seed=rows, base=0.0, grow=grow)
+        b.scales = [torch.full_like(s, scale) for s in b.scales]
+        pc, (table, lens, cu) = b.cache(), b.dev()
+        nsnq.nsnq_paged_append(b.k.cuda(), b.v.cuda(), pc, table, lens, cu, rope_base=b.base)
+        codes, scales = b.stored()
+        OP.append(b.k.double().numpy(), b.v.double().numpy(), codes, scales, b.table.tolist(), b.lens, b.cu, b.base)
+        check_pool(pc, codes, scales)
+
+
+@pytest.mark.parametrize("rows", [1, 4, 70])
+@pytest.mark.parametrize("scale", [1e-40, 2.0 ** -140, 2.0 ** -126])
+def test_attention_under_extreme_scales_of_a_caller(rows, scale):
+    """Value scales below fp32's normal range: finite results, within half a step of what the type holds there (fp32
+    subnormals: 2^-150 for a part, its factor and the sum of each of up to 130 tokens). For bf16 a weight times a v
+    scale below 2^-118 is held in steps of 2^-23 of that: off by 2^-142 each, times a code of at most 448."""
+    b = Batch([rows], [60], 4, 2, 16, seed=rows)
+    b.scales[1].fill_(scale)
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=rows, out_dtype=torch.float32).double().cpu().numpy()
+    codes, scales = b.stored()
+    want, weight, reach, _ = OP.attention(b.q.double().numpy(), codes, scales, b.table.tolist(), b.lens, b.cu, 0, 0,
+                                          1 / math.sqrt(D))
+    e = 2.0 ** -18 + 160 * 2.0 ** -23 * reach[..., None]
+    assert (np.abs(got - want) <= 2 * e * weight + 2.0 ** -24 * np.abs(want) + 200 * 2.0 ** -149).all()
+    got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=rows).double().cpu().numpy()
+    assert (np.abs(got - want) <= 2 * (e + 2.0 ** -11) * weight + 2.0 ** -8 * np.abs(want) + 2.0 ** -133 + (60 + rows) * 448 * 2.0 ** -142).all()
