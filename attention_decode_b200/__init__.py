@@ -744,14 +744,16 @@ def nsnq_paged_attn_workspace(n_rows: int, B: int, Hq: int, Hkv: int, max_rows: 
 
 
 def nsnq_paged_attn(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
-                    cu_rows: Optional[torch.Tensor] = None, max_rows: int = 1, window: int = 0,
+                    cu_rows: Optional[torch.Tensor] = None, max_rows: Optional[int] = None, window: int = 0,
                     sinks: int = 0, softmax_scale: float = 0.0,
                     out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal attention of the packed rows q [rows][Hq][D] (rotated, fp32 or bf16),
     the last tokens of their sequences, over the paged cache: returns
-    [rows][Hq][D]. max_rows bounds the rows of a sequence. With window > 0 a
-    row sees the last `window` tokens up to its own and the first `sinks`."""
+    [rows][Hq][D]. max_rows bounds the rows of a sequence (without it, one row
+    without cu_rows, all rows with them: give the real bound, small counts run on
+    a faster kernel and need less workspace). With window > 0 a row sees the last
+    `window` tokens up to its own and the first `sinks`."""
     c, index = cache._c(), q.get_device()
     N, Hq, D = q.shape
     q_t, q_h, q_d = q.stride()
@@ -759,6 +761,8 @@ def nsnq_paged_attn(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
         raise ValueError("q must have contiguous channels and be on the cache's device")
     code = _dtype_code(q)
     B, cols, row_stride, cu = _paged_seqs(index, N, page_table, seq_lens, cu_rows)
+    if max_rows is None:
+        max_rows = 1 if cu is None else N
     if out is not None and (out.shape != q.shape or out.get_device() != index or not out.is_contiguous()):
         raise ValueError("out must be contiguous, of q's shape")
     if workspace is not None and workspace.get_device() != index:

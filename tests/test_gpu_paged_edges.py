@@ -271,3 +271,12 @@ def test_attention_under_extreme_scales_of_a_caller(rows, scale):
     assert (np.abs(got - want) <= 2 * e * weight + 2.0 ** -24 * np.abs(want) + 200 * 2.0 ** -149).all()
     got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=rows).double().cpu().numpy()
     assert (np.abs(got - want) <= 2 * (e + 2.0 ** -11) * weight + 2.0 ** -8 * np.abs(want) + 2.0 ** -133 + (60 + rows) * 448 * 2.0 ** -142).all()
+
+
+def test_rows_of_a_sequence_without_max_rows():
+    """cu_rows without max_rows: every row is attended, as with the largest count given."""
+    b = Batch([6, 1, 30], [3, 70, 0], 4, 2, 16, seed=7)
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu)
+    bounded(got, b.q, b, *b.stored())
+    pc.check()
