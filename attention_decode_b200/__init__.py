@@ -578,12 +578,16 @@ class PagedCache:
     float8_e4m3fn, k_scales, v_scales [num_pages][Hkv] fp32 (value = code *
     scale). status is an int32 word in which the kernels report what they left
     out (PAGED_BAD_PAGE, PAGED_BAD_LENGTH) or that a call's outputs are void
-    (PAGED_TIMEOUT); check() reads it."""
+    (PAGED_TIMEOUT); check() reads it. One is made where none is given."""
     k: torch.Tensor
     v: torch.Tensor
     k_scales: torch.Tensor
     v_scales: torch.Tensor
     status: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        if self.status is None:
+            self.status = torch.zeros(1, dtype=torch.int32, device=self.k.device)
 
     @property
     def num_pages(self) -> int:

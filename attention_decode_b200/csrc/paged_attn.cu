@@ -346,12 +346,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     PagedWalk<RC, kSetup> walk(a, ms.range);
     const int G = (int)a.G.d;
     const int slots = kTile / a.page;
-    if (blockIdx.x == 0 && warp == 4 && a.seqs.status)
-#pragma unroll 1
-        for (int i = lane; i < a.seqs.B; i += 32) {
-            const PagedSeq q = paged_seq(a.seqs, i);
-            paged_report(a.seqs, q.bad | (q.rows > a.max_rows ? kBadLength : 0u));
-        }
     Waiter wait;
     uint32_t it = 0;  // tiles of this CTA so far
 

@@ -61,7 +61,7 @@ constexpr int kMaxParts = 640;  // CTAs of the largest grid (two per SM of up to
 // (a long context over every CTA): the four warps then share a row's parts, in
 // a fixed order. A unit of many rows is in two or three: a warp takes a row.
 // Block (grid + b, y): zeros for the rows of sequence b in front of its first
-// token.
+// token, and the report of its lengths.
 template <int RC>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
     constexpr int kWarps = kJoinThreads / 32, kShare = RC <= 16 ? kWarps : 1;  // warps to a row
@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((int)blockIdx.x >= grid) {
         const PagedSeq s = paged_seq(a.seqs, blockIdx.x - grid);
+        if (blockIdx.y == 0 && threadIdx.x == 0) paged_report(a.seqs, s.bad | (s.rows > a.max_rows ? kBadLength : 0u));
         const int64_t rows = s.rows < a.max_rows ? s.rows : a.max_rows;
         const int64_t blind = s.rows - s.len < rows ? s.rows - s.len : rows;
 #pragma unroll 1

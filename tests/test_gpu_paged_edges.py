@@ -280,3 +280,17 @@ def test_rows_of_a_sequence_without_max_rows():
     got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu)
     bounded(got, b.q, b, *b.stored())
     pc.check()
+
+
+def test_a_cache_of_a_callers_own_tensors_reports():
+    b = Batch([2, 2], [3, 70], 4, 2, 16, seed=8)
+    full, (table, lens, cu) = b.cache(), b.dev()
+    pc = nsnq.PagedCache(full.k, full.v, full.k_scales, full.v_scales)
+    table[1, 4] = -1
+    nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=2)
+    with pytest.raises(nsnq.NSNQError, match="page table"):
+        pc.check()
+    lens[0] = 10 ** 6
+    nsnq.nsnq_paged_append(b.k.cuda(), b.v.cuda(), pc, table.clamp(0), lens, cu)
+    with pytest.raises(nsnq.NSNQError, match="lengths"):
+        pc.check()
