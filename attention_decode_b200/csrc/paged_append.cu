@@ -129,17 +129,32 @@ __device__ __forceinline__ int last_at_most(int B, int64_t x, Key key) {
 // blocks of sequence b begin at cu_rows[b] / page + 2 b, found without a walk
 // over the sequences before it (with a walk 8192 sequences of 4 rows, pages of
 // 64, took 13.2 ms, now 1.4; 1024 of them 349 and 179 us; 8 x 4096 rows the same).
-// False for a block that is left over.
+// False for a block that is left over, and for one of a sequence that is left
+// out (seq.len < seq.rows), whose slots are its rows page by page from `slot` 0 on.
 __device__ __forceinline__ bool find_item(const PagedSeqs& s, int page, int64_t item, int& b, int& slot,
                                           PagedSeq& seq) {
-    auto begin = [&](int i) { return (int64_t)(s.cu_rows ? s.cu_rows[i] : i) / page + 2 * (int64_t)i; };
+    auto begin = [&](int i) {
+        const int64_t row = s.cu_rows ? s.cu_rows[i] : i;
+        return (row < 0 ? 0 : row > s.n_rows ? s.n_rows : row) / page + 2 * (int64_t)i;
+    };
     b = last_at_most(s.B, item, begin);
     seq = paged_seq(s, b);
+    slot = (int)(item - begin(b));
     if (seq.rows == 0 || seq.len < seq.rows) return false;
     const int first = (seq.len - seq.rows) / page, n = (seq.len - 1) / page - first + 1;
     const int64_t at = item - begin(b);
     slot = first + (int)at;
     return at >= 0 && at < n;
+}
+
+// Zeros for query head h of packed rows [r0, r1), a warp's eight bytes a lane.
+template <typename XT>
+__device__ __forceinline__ void clear_rows(const PagedAppendArgs& a, int64_t r0, int64_t r1, int h) {
+    constexpr int kBytes = kD * sizeof(XT);
+    for (int64_t r = r0; r < r1; ++r) {
+        char* at = reinterpret_cast<char*>(a.q_out) + (r * a.Hq + h) * kBytes;
+        for (int i = 8 * lane_id(); i < kBytes; i += 256) *reinterpret_cast<uint2*>(at + i) = make_uint2(0, 0);
+    }
 }
 
 // The codes of an older row under a grown scale: old codes are worth `ratio` new ones.
@@ -179,10 +194,18 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
         for (int b = threadIdx.x; b < a.seqs.B; b += kThreads) paged_report(a.seqs, paged_seq(a.seqs, b).bad);
     int b = 0, slot = 0;
     PagedSeq seq{};
-    if (!find_item(a.seqs, PAGE, item, b, slot, seq)) return;
+    const bool live = find_item(a.seqs, PAGE, item, b, slot, seq);
     const int kind = group < gkv ? 0 : group < 2 * gkv ? 1 : 2;  // K, V, Q
     const int h0 = (group - kind * gkv) * a.heads, H = kind == 2 ? a.Hq : a.Hkv;
     const int h1 = h0 + a.heads < H ? h0 + a.heads : H;
+    if (!live) {
+        if (kind == 2 && seq.len < seq.rows && slot >= 0 && (int64_t)slot * PAGE < seq.rows) {
+            const int n = seq.rows - slot * PAGE < PAGE ? seq.rows - slot * PAGE : PAGE;
+            for (int h = h0 + warp; h < h1; h += kWarps)
+                clear_rows<XT>(a, (int64_t)seq.row0 + slot * PAGE, (int64_t)seq.row0 + slot * PAGE + n, h);
+        }
+        return;
+    }
     const int start = seq.len - seq.rows, t0 = slot * PAGE;
     const int first = start > t0 ? start - t0 : 0;  // page row of the first new token
     const int last = seq.len - t0 < PAGE ? seq.len - t0 : PAGE;
@@ -402,7 +425,11 @@ __global__ void __launch_bounds__(128) paged_append_few_kernel(const __grid_cons
     if (row >= a.seqs.n_rows) return;
     int b = 0;
     PagedSeq seq{};
-    if (!find_row(a.seqs, (int)row, b, seq)) return;
+    if (!find_row(a.seqs, (int)row, b, seq)) {
+        const int h = (int)(w % heads) - 2 * a.Hkv;
+        if (h >= 0 && row >= seq.row0 && row < seq.row0 + seq.rows) clear_rows<XT>(a, row, row + 1, h);  // left out
+        return;
+    }
     const int pos = seq.len - seq.rows + (int)row - seq.row0, slot = pos / a.page;
     if (row > seq.row0 && pos % a.page) return;  // an earlier row's page
     const int hh = (int)(w % heads), kind = hh < a.Hkv ? 0 : hh < 2 * a.Hkv ? 1 : 2;  // K, V, Q

@@ -449,8 +449,8 @@ typedef enum {
  * that holds older tokens of the sequence keep its scale if they fit under
  * it; else the scale grows and the page's older codes are rounded again to
  * the new one (exact but for codes that fall below e4m3's normal range).
- * Rows behind the new tokens are left as they were, and so are q_out rows of
- * sequences reported as NSNQ_PAGED_BAD_LENGTH. Pages that several sequences
+ * Rows behind the new tokens are left as they were. q_out rows of sequences
+ * reported as NSNQ_PAGED_BAD_LENGTH become zeros. Pages that several sequences
  * of a call write to are the caller's error (their contents are then any mix
  * of both).
  * B, Hq, Hkv <= 65535, n_rows * max(Hq, Hkv) < 2^31 (NSNQ_ERR_UNSUPPORTED

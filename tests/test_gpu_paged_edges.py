@@ -142,18 +142,23 @@ def test_appends_with_and_without_rotation_in_either_order(first, second, page, 
     assert run.returncode == 0 and "both orders fine" in run.stdout, run.stderr[-2000:]
 
 
-@pytest.mark.parametrize("cu,lens", [([0, 10], [20]), ([-2, 6], [20]), ([0, 3, 12], [9, 30]), ([0, 5, 3, 8], [9, 9, 9]),
+@pytest.mark.parametrize("cu,lens", [([0, 10], [20]), ([-2, 6], [20]), ([-1000, 6, 8], [20, 9]), ([0, 3, 12], [9, 30]), ([0, 5, 3, 8], [9, 9, 9]),
                                      ([0, 1000000], [20]), ([0, 2, 40, 42], [7, 60, 8]), ([0, 2, 4, 6, 7, 20], [9, 20, 33, 17, 50])])
 def test_rows_out_of_range_are_left_out(cu, lens):
-    """A sequence whose rows the row tensors do not hold: nothing stored, nothing attended."""
+    """A sequence whose rows the row tensors do not hold: nothing stored, zeros for the rows that there are."""
     B, n = len(lens), 8
     b = Batch([n] * B, [40] * B, 4, 2, 16, seed=B)
     pc, table = b.cache(), b.table.cuda()
     q, k, v = (x[:n].cuda() for x in (b.q, b.k, b.v))
     good = [s for s in range(B) if 0 <= cu[s] <= cu[s + 1] <= n]
     bad = [s for s in range(B) if s not in good]
-    nsnq.nsnq_paged_append(k, v, pc, table, i32(lens), i32(cu), q=q, rope_base=b.base)
+    qr = torch.full_like(q, 7.0)
+    nsnq.nsnq_paged_append(k, v, pc, table, i32(lens), i32(cu), q=q, q_out=qr, rope_base=b.base)
     assert int(pc.status) == nsnq.PAGED_BAD_LENGTH
+    for s in bad:
+        lo, hi = max(0, min(n, cu[s])), max(0, min(n, cu[s + 1]))
+        if cu != [0, 5, 3, 8]:
+            assert (qr[lo:hi] == 0).all()
     codes, scales = b.stored()
     for s in good:
         if cu != [0, 5, 3, 8]:                     # (overlapping rows: each sequence stores its own)
@@ -294,3 +299,28 @@ def test_a_cache_of_a_callers_own_tensors_reports():
     nsnq.nsnq_paged_append(b.k.cuda(), b.v.cuda(), pc, table.clamp(0), lens, cu)
     with pytest.raises(nsnq.NSNQError, match="lengths"):
         pc.check()
+
+
+@pytest.mark.parametrize("rows", [1, 3, 40])
+def test_rows_left_out_hold_zeros(rows):
+    """Rows of a sequence whose length is out of range: zeros in the queries and in the outputs of the calls."""
+    b = Batch([rows] * 3, [3, 70, 40], 4, 2, 16, seed=rows)
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    for bad in (10 ** 6, -1, rows - 1):
+        lens[1] = bad
+        qr = torch.full_like(b.q, 7.0).cuda()
+        nsnq.nsnq_paged_append(b.k.cuda(), b.v.cuda(), pc, table, lens, cu, q=b.q.cuda(), q_out=qr, rope_base=b.base)
+        assert (qr[rows:2 * rows] == 0).all() and (qr[:rows] != 0).any() and (qr[2 * rows:] != 0).any()
+        out = torch.full_like(b.q, 7.0).cuda()
+        nsnq.nsnq_paged_attn(qr, pc, table, lens, cu, max_rows=rows, out=out)
+        assert (out[rows:2 * rows] == 0).all() if bad != rows - 1 else (out[rows] == 0).all()
+
+
+def test_rows_that_no_call_can_reach_hold_zeros():
+    """An output made by the call, more rows in it than max_rows of every sequence can be: the rest is zero."""
+    b = Batch([2, 2], [3, 70], 4, 2, 16, seed=9, spare_rows=60)
+    pc, (table, lens, cu) = b.cache(), b.dev()
+    for _ in range(3):
+        torch.full((64, 4, D), 7.0, dtype=torch.bfloat16, device="cuda")  # what the allocator may hand out again
+        got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=2)
+        assert (got[4:] == 0).all()
