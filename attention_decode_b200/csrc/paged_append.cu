@@ -9,10 +9,14 @@
 //
 // Codes and scales are those of the fp64 rotation, decided in fp32: angles are
 // reduced in fp64, cos and sin rounded to fp32, and a rotated value is then
-// off by at most 2^-22 (|x| + |y|) of its pair (x, y). Where a code or scale
+// off by at most 2^-21.8 (|x| + |y|) of its pair (x, y): 2^-24 each for cos or sin
+// and its angle, the product and the sum. Where a code or scale
 // would change within twice that, it is decided again from an fp64 rotation
 // (about one code in 10^5). The cos and sin of a page's rows are computed once
-// per block, in shared memory, and serve all its heads.
+// per block, in shared memory, and serve all its heads. Queries are not decisions:
+// bf16 ones are rounded from the fp32 rotation (deciding again where that is not
+// sure of the nearest bf16 took 257 us instead of 181 below, for one bit in 3 *
+// 10^4 values), fp32 ones from one in two words (22 -> 25 us, 5 x ~580 rows).
 //
 // What bounds it: memory, in the end (a row is read once and written once; the
 // next heads' rows are copied to shared memory ahead by cp.async). A prompt of
@@ -38,7 +42,7 @@ struct AppShape {
 // Heads whose rows a block has on their way or at hand.
 template <typename XT>
 constexpr int app_ahead() { return sizeof(XT) == 2 ? 3 : 2; }
-constexpr float kErr = 0x1p-20f;  // of |lo| + |hi|, rotated: >= 2^-22 (|x| + |y|) twice over
+constexpr float kErr = 0x1p-20f;  // of |lo| + |hi|, rotated: >= 2^-21.8 (|x| + |y|) and as much again
 
 // The least e >= -126 with a <= 448 * 2^e, for finite a >= 0:
 // a = f * 2^k with 1 <= f < 2, and 448 = 1.75 * 2^8.
@@ -87,10 +91,15 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {  // the low half holds a
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+    for (int i = 0; i < 4; ++i) u[i] = bf16x2(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
@@ -107,6 +116,16 @@ __device__ __noinline__ double2 exact_pair(float x, float y, int t, double freq)
     double s, c;
     sincos((double)t * freq, &s, &c);
     return make_double2((double)x * c - (double)y * s, (double)x * s + (double)y * c);
+}
+
+// x c + y s for c = ch + cl and s = sh + sl to 2^-48, rounded to fp32 once but for
+// that: products and their sum with what their roundings leave out.
+__device__ __forceinline__ float rotated_once(float x, float ch, float cl, float y, float sh, float sl) {
+    const float p = __fmul_rn(x, ch), q = __fmul_rn(y, sh), v = __fadd_rn(p, q);
+    if (!isfinite(v)) return v;
+    const float b = __fsub_rn(v, p), rest = __fadd_rn(__fsub_rn(p, __fsub_rn(v, b)), __fsub_rn(q, b));
+    const float low = __fadd_rn(fmaf(x, ch, -p), fmaf(y, sh, -q));
+    return __fadd_rn(v, __fadd_rn(rest, __fadd_rn(low, fmaf(x, cl, __fmul_rn(y, sl)))));
 }
 
 // The last sequence b with key(b) <= x (the first, if none has), for a key that
@@ -222,6 +241,43 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
     const int64_t sh = kind == 0 ? a.k_sh : kind == 1 ? a.v_sh : a.q_sh;
     const XT* x0 = reinterpret_cast<const XT*>(kind == 0 ? a.k : kind == 1 ? a.v : a.q);
     const int64_t row0 = seq.row0 + t0 - start;  // packed row of page row 0
+    if (sizeof(XT) == 4 && kind == 2 && rope) {
+        // fp32 queries keep their 24 bits: a thread holds the angles of a row's
+        // channels in two words each and takes the row's heads one after the other.
+#pragma unroll 1
+        for (int r = rg; r < last; r += kThreads / 8) {
+            if (r < first) continue;
+            float ch[8], cl[8], sh_[8], sl[8];
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                double s, c;
+                sincospi(2.0 * (t0 + r) * a.turns[8 * l + i], &s, &c);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k == i) {
+                        ch[k] = (float)c, cl[k] = (float)(c - (double)ch[k]);
+                        sh_[k] = (float)s, sl[k] = (float)(s - (double)sh_[k]);
+                    }
+            }
+#pragma unroll 2
+            for (int h = h0; h < h1; ++h) {
+                const XT* from = x0 + h * sh + (row0 + r) * st + 8 * l;
+                float x[8], y[8];
+                load8f(from, x);
+                load8f(from + kD / 2, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float u = rotated_once(x[i], ch[i], cl[i], y[i], -sh_[i], -sl[i]);
+                    y[i] = rotated_once(x[i], sh_[i], sl[i], y[i], ch[i], cl[i]);
+                    x[i] = u;
+                }
+                XT* o = reinterpret_cast<XT*>(a.q_out) + ((row0 + r) * a.Hq + h) * kD + 8 * l;
+                store8(o, x);
+                store8(o + kD / 2, y);
+            }
+        }
+        return;
+    }
     // The rows of the next heads are on their way to shared memory; a thread
     // reads only what it copied itself.
     XT* ring = reinterpret_cast<XT*>(cs + (a.rope ? PAGE * 64 : 0));
@@ -480,7 +536,10 @@ __global__ void __launch_bounds__(128) paged_append_few_kernel(const __grid_cons
             XT* o = reinterpret_cast<XT*>(a.q_out) + ((row0 + r) * a.Hq + h) * kD + 8 * l;
             float u[8], v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = (float)lo[i], v[i] = (float)hi[i];
+            for (int i = 0; i < 8; ++i) {  // (to odd: the only rounding is the store's)
+                u[i] = sizeof(XT) == 2 ? to_odd(lo[i]) : (float)lo[i];
+                v[i] = sizeof(XT) == 2 ? to_odd(hi[i]) : (float)hi[i];
+            }
             store8(o, u);
             store8(o + kD / 2, v);
         }

@@ -436,7 +436,11 @@ typedef enum {
  *          strides (elements; channels contiguous, rows 16-byte aligned).
  *   q      device [n_rows][Hq][D] likewise, or NULL: rotated like the keys
  *          into q_out [n_rows][Hq][D] (contiguous, of dtype; may equal a
- *          contiguous q), each value rounded once. Hq is ignored without q.
+ *          contiguous q). fp32: the fp64 value rounded once. bf16: the same
+ *          in calls of up to two rows per sequence on average; with more
+ *          rows it is rotated in fp32, and a value within 2^-21 (|x_i| +
+ *          |x_{i+D/2}|) of the middle between two bf16 numbers may become
+ *          the other one. Hq is ignored without q.
  *   rope_base  0: no rotation (q_out is then a copy of q). Else finite, > 1:
  *          (x_i, x_{i+D/2}) -> (x_i c - x_{i+D/2} s, x_i s + x_{i+D/2} c),
  *          c, s = cos, sin of t * rope_base^(-2i/D), i < D/2, at token t.

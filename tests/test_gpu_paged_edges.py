@@ -324,3 +324,32 @@ def test_rows_that_no_call_can_reach_hold_zeros():
         torch.full((64, 4, D), 7.0, dtype=torch.bfloat16, device="cuda")  # what the allocator may hand out again
         got = nsnq.nsnq_paged_attn(b.q.cuda(), pc, table, lens, cu, max_rows=2)
         assert (got[4:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("page,base,before", [(64, 10000.0, 0), (16, 500.0, 4000), (128, 1e6, 100000)])
+def test_queries_are_rounded_once(page, base, before, dtype):
+    """The rotation in fp64 and one rounding, whichever kernel the number of rows selects: half a step of the
+    result's own binade, and 2^-30 (|a| + |b|) of an angle's fp64 error at the longest position here (2^17 * 2^-53
+    twice over, and the sine's own). Many bf16 rows are rotated in fp32: 2^-21 (|a| + |b|) in its place."""
+    rows, hq = 150, 12
+    g = torch.Generator().manual_seed(page)
+    q = torch.randn(rows, hq, D, generator=g).to(dtype)
+    kv = torch.randn(rows, 1, D, generator=g).to(dtype).cuda()
+    pages = -(-(before + rows) // page)
+    pc = nsnq.PagedCache.empty(pages, 1, page)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    got = nsnq.nsnq_paged_append(kv, kv, pc, table, i32([before + rows]), i32([0, rows]), q=q.cuda(), rope_base=base)
+    each = torch.cat([nsnq.nsnq_paged_append(kv[i:i + 1], kv[i:i + 1], pc, table, i32([before + i + 1]),
+                                             q=q[i:i + 1].cuda(), rope_base=base) for i in range(rows)])
+    x = q.double().numpy()
+    want = np.stack([OP.rotate(x[i], before + i, base) for i in range(rows)])
+    size = np.abs(x[..., :64]) + np.abs(x[..., 64:])
+    step = np.exp2(np.floor(np.log2(np.maximum(np.abs(want), 1e-30)))) * torch.finfo(dtype).eps
+    size = np.concatenate((size, size), -1)
+    for out, extra in ((got, -21 if dtype == torch.bfloat16 else -30), (each, -30)):
+        tol = step / 2 + 2.0 ** extra * size
+        err = np.abs(out.double().cpu().numpy() - want)
+        assert (err <= tol).all(), (np.argwhere(err > tol).shape, (err / tol).max())
+    if dtype == torch.float32:
+        assert (got != each).sum() <= got.numel() * 2.0 ** -18  # fp64 values on a border alone
