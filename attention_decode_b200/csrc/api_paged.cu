@@ -67,7 +67,10 @@ nsnq_status check_paged(const nsnq_paged_cache& c, const int32_t* cu_rows, const
     return NSNQ_OK;
 }
 
-nsnq_status check_rows(const void* p, const char* name, int64_t st, int64_t sh, int64_t esz) {
+// (the stride of a dimension of one element is never used, and may be any)
+nsnq_status check_rows(const void* p, const char* name, int64_t n_rows, int heads, int64_t st, int64_t sh, int64_t esz) {
+    if (n_rows == 1) st = 0;
+    if (heads == 1) sh = 0;
     if (!p) return set_error(NSNQ_ERR_INVALID_ARG, "%s is NULL", name);
     if (!aligned(p, 16) || (st * esz) % 16 || (sh * esz) % 16)
         return set_error(NSNQ_ERR_INVALID_ARG, "%s and its strides must be 16-byte aligned", name);
@@ -97,13 +100,13 @@ nsnq_status nsnq_paged_append(const void* k, const void* v, const void* q, void*
     if (s != NSNQ_OK) return s;
     if (B == 0 || n_rows == 0) return ok();
     const int64_t esz = dtype == NSNQ_BF16 ? 2 : 4;
-    s = check_rows(k, "k", k_stride_t, k_stride_h, esz);
-    if (s == NSNQ_OK) s = check_rows(v, "v", v_stride_t, v_stride_h, esz);
-    if (s == NSNQ_OK && q) s = check_rows(q, "q", q_stride_t, q_stride_h, esz);
+    s = check_rows(k, "k", n_rows, Hkv, k_stride_t, k_stride_h, esz);
+    if (s == NSNQ_OK) s = check_rows(v, "v", n_rows, Hkv, v_stride_t, v_stride_h, esz);
+    if (s == NSNQ_OK && q) s = check_rows(q, "q", n_rows, Hq, q_stride_t, q_stride_h, esz);
     if (s != NSNQ_OK) return s;
     if (q && (!q_out || !aligned(q_out, 16)))
         return set_error(NSNQ_ERR_INVALID_ARG, "q_out is NULL or not 16-byte aligned");
-    if (q && q == q_out && (q_stride_t != (int64_t)Hq * D || q_stride_h != D))
+    if (q && q == q_out && ((n_rows > 1 && q_stride_t != (int64_t)Hq * D) || (Hq > 1 && q_stride_h != D)))
         return set_error(NSNQ_ERR_INVALID_ARG, "q_out may equal q only if q is contiguous");
     a.k = k; a.v = v; a.q = q; a.q_out = q_out;
     a.k_st = k_stride_t; a.k_sh = k_stride_h;
@@ -150,7 +153,7 @@ nsnq_status nsnq_paged_attn(const void* q, nsnq_dtype q_dtype, int64_t n_rows, i
     if (max_rows < 0) return set_error(NSNQ_ERR_INVALID_ARG, "max_rows = %lld < 0", (long long)max_rows);
     if (!isfinite(softmax_scale)) return set_error(NSNQ_ERR_INVALID_ARG, "softmax_scale is not finite");
     if (B == 0 || n_rows == 0 || max_rows == 0) return ok();
-    s = check_rows(q, "q", q_stride_t, q_stride_h, q_dtype == NSNQ_BF16 ? 2 : 4);
+    s = check_rows(q, "q", n_rows, Hq, q_stride_t, q_stride_h, q_dtype == NSNQ_BF16 ? 2 : 4);
     if (s != NSNQ_OK) return s;
     if (!out || !aligned(out, 16)) return set_error(NSNQ_ERR_INVALID_ARG, "out is NULL or not 16-byte aligned");
     const size_t need = nsnq::paged_attn_workspace(n_rows, B, Hq, Hkv, max_rows);

@@ -353,3 +353,22 @@ def test_queries_are_rounded_once(page, base, before, dtype):
         assert (err <= tol).all(), (np.argwhere(err > tol).shape, (err / tol).max())
     if dtype == torch.float32:
         assert (got != each).sum() <= got.numel() * 2.0 ** -18  # fp64 values on a border alone
+
+
+def test_strides_of_a_single_row_or_head_do_not_count():
+    """A dimension of one element is never stepped over: any stride, also that of an in-place single row."""
+    b = Batch([1], [20], 4, 1, 16, seed=3)
+    (table, lens, _), n = b.dev(), 6 * D + 3
+    fused = torch.zeros(1, n, dtype=torch.bfloat16, device="cuda")
+    fused[:, :6 * D] = torch.cat((b.q.flatten(1), b.k.flatten(1), b.v.flatten(1)), 1).cuda()
+    q = fused.as_strided((1, 4, D), (n, D, 1))
+    k, v = (fused.as_strided((1, 1, D), (n, 7, 1), at * D) for at in (4, 5))
+    want = nsnq.nsnq_paged_append(b.k.cuda(), b.v.cuda(), b.cache(), table, lens, q=b.q.cuda(), rope_base=b.base)
+    pc = b.cache()
+    assert nsnq.nsnq_paged_append(k, v, pc, table, lens, q=q, q_out=q, rope_base=b.base) is q
+    assert torch.equal(q, want)
+    codes, scales = b.stored()
+    OP.append(b.k.double().numpy(), b.v.double().numpy(), codes, scales, b.table.tolist(), b.lens, b.cu, b.base)
+    check_pool(pc, codes, scales)
+    got = nsnq.nsnq_paged_attn(q, pc, table, lens)
+    assert torch.equal(got, nsnq.nsnq_paged_attn(want, pc, table, lens))
