@@ -620,15 +620,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (r >= u.rows) continue;
                 const float m = __shfl_sync(kFull, state.m, r), vref = power_of_two(-__shfl_sync(kFull, state.lrv, r));
                 const float sum = ms.sums[0][r] + ms.sums[1][r] + ms.sums[2][r] + ms.sums[3][r];
-                float v = o[r];
+                float v = sum == 0.f ? 0.f : o[r] / sum * vref;
                 if ((ms.nan[r][tid >> 5] >> (tid & 31)) & 1u) v = NAN;
                 if (!complete) {
-                    part[r * kD + tid] = v * vref;
+                    part[r * kD + tid] = v;
                     if (tid == 0) part[RC * kD + r] = m, part[RC * kD + RC + r] = sum;
                     continue;
                 }
                 const int rr = u.r0 + r, i = (int)fdiv((uint32_t)rr, a.G);
-                store_out(a, (int64_t)(u.row0 + i) * a.Hq + walk.h * G + rr - i * G, tid, sum == 0.f ? 0.f : v / sum * vref);
+                store_out(a, (int64_t)(u.row0 + i) * a.Hq + walk.h * G + rr - i * G, tid, v);
             }
         }
     }

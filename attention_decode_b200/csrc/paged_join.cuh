@@ -13,8 +13,9 @@ namespace nsnq {
 cudaError_t launch_paged_rows(const PagedAttnArgs& a, cudaStream_t s);
 size_t paged_rows_workspace();
 
-// A part of a unit of RC rows: [RC][128] sums, [RC] m, [RC] l. A CTA leaves at
-// most two: slot 2c for the unit its range begins in, 2c + 1 for a later one.
+// A part of a unit of RC rows: [RC][128] outputs over the part's tokens alone (of
+// the values' own size, whatever the scales), [RC] m, [RC] l, the sum of the
+// weights relative to 2^m. A CTA leaves at most two: slot 2c for the unit its range begins in, 2c + 1 for a later one.
 template <int RC>
 __host__ __device__ constexpr int64_t part_stride() { return RC * (kD + 2); }
 
@@ -95,12 +96,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     for (int k = lane; k < n; k += 32) {
         const float* p = part(k) + RC * kD + r;
         const float m = p[0], l = p[RC];
-        const float f = l != 0.f ? exp2_approx(m - top) : -1.f;  // -1: the row sees nothing of the part
+        const float f = l != 0.f ? exp2_approx(m - top) * l : -1.f;  // -1: the row sees nothing of the part
         if (k % kShare == w0) factor[warp][k / kShare] = f;
-        if (l != 0.f) sum = fmaf(f, l, sum);
+        if (l != 0.f) sum += f;
     }
     sum = warp_sum(sum);
     __syncwarp();
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int k = w0; k < n; k += kShare) {
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // a factor of 0 keeps the part's NaN, and nothing else of it
-            if (f != -1.f && (f != 0.f || isnan(w[i]))) acc[i] = fmaf(f, w[i], acc[i]);
+            if (f != -1.f && (f != 0.f || isnan(w[i]))) acc[i] = fmaf(f * inv, w[i], acc[i]);
     }
     if (kShare > 1) {
         sums[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -123,8 +125,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     }
     const int rr = seam.r0 + r, i = (int)fdiv((uint32_t)rr, a.G), G = (int)a.G.d;
     const int64_t at = ((int64_t)(seam.row0 + i) * a.Hq + seam.h * G + rr - i * G) * kD + 4 * lane;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = sum == 0.f ? 0.f : acc[k] / sum;
     if (a.out_bf16)
         *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at) =
             make_uint2((uint32_t)f32_to_bf16_rn(acc[0]) | ((uint32_t)f32_to_bf16_rn(acc[1]) << 16),

@@ -244,7 +244,8 @@ __device__ __forceinline__ void row_weights(const uint32_t (&u)[16], uint32_t se
 // weight x v scale there, and scales those rows' weights and outputs so far;
 // returns the new maximum and reference and the factor of the sum of weights. The
 // reference is a page's v scale itself where the largest weight lies there
-// (weights need no factor then), and at least 2^-126: its reciprocal is finite.
+// (weights need no factor then), and from 2^-126 to 2^126: its reciprocal is a
+// normal number.
 // Calls are rare, but all warps of a half wait for one: of the step's columns
 // rather than the 16 at hand, and with a wide lag, a third as many are needed.
 __device__ __noinline__ float3 raise_row(uint32_t s, uint32_t o, bool have_o, int q, int b, uint32_t seen0, uint32_t seen1,
@@ -271,7 +272,7 @@ __device__ __noinline__ float3 raise_row(uint32_t s, uint32_t o, bool have_o, in
         }
     }
     const float f = m == mn ? 1.f : exp2_approx(m - mn), old = vref * f;
-    vn = need ? fmaxf(fmaxf(old, vn), 0x1p-126f) : vref;
+    vn = need ? fminf(fmaxf(fmaxf(old, vn), 0x1p-126f), 0x1p126f) : vref;
     const float fo = vn == old ? 1.f : old / vn;
     if (__any_sync(kFull, fo != 1.f)) rescale_row(s, 8 * q, o, have_o, fo);
     return make_float3(mn, vn, f);
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const bool complete = walk.complete();
                 float* part = a.part + (2 * blockIdx.x + (walk.first ? 0 : 1)) * part_stride<RC>();
-                const float inv = complete ? (st.l == 0.f ? 0.f : 1.f / st.l) : 1.f;
+                const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
                 __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + out_row * kD;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {

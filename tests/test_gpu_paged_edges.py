@@ -13,7 +13,7 @@ import torch
 
 import attention_decode_b200 as nsnq
 from oracle import paged as OP
-from test_gpu_paged import Batch, D, check_pool
+from test_gpu_paged import Batch, D, check_pool, dense64
 
 pytestmark = pytest.mark.gpu
 
@@ -372,3 +372,21 @@ def test_strides_of_a_single_row_or_head_do_not_count():
     check_pool(pc, codes, scales)
     got = nsnq.nsnq_paged_attn(q, pc, table, lens)
     assert torch.equal(got, nsnq.nsnq_paged_attn(want, pc, table, lens))
+
+
+@pytest.mark.parametrize("rows,dtype", [(1, torch.bfloat16), (6, torch.bfloat16), (40, torch.bfloat16), (2, torch.float32)])
+@pytest.mark.parametrize("exponent", [105, 119, -120])
+def test_values_near_the_ends_of_the_range_over_many_ctas(rows, dtype, exponent):
+    """Value scales near both ends of fp32, a context that many CTAs share: each part is of the values' own size."""
+    b = Batch([rows], [30000], 4, 1, 128, dtype, seed=rows)
+    b.scales[1].copy_(torch.exp2(exponent - torch.randint(0, 2, b.scales[1].shape, generator=torch.Generator().manual_seed(1))))
+    b.codes[1] = (b.codes[1].int() % 0x70 + (b.codes[1].int() & 0x80)).to(torch.uint8)   # at most 240: finite sums of two
+    pc, (table, lens, cu), q = b.cache(), b.dev(), b.q.cuda()
+    got = nsnq.nsnq_paged_attn(q, pc, table, lens, cu, max_rows=rows, out_dtype=dtype).double()
+    want, weight, reach, _ = dense64(q, b, pc, table, 0, 0, 1 / math.sqrt(D))
+    e = 2.0 ** -18 + 160 * 2.0 ** -23 * reach + (2.0 ** -10 if dtype == torch.bfloat16 else 0.0)
+    # besides, of each token half a step of 2^-23 of the largest product (at most 2^exponent), over a sum of weights of
+    # at least 1, times a code; below 2^-118, of that; and fp32's own steps under its normal range
+    lost = lens[0].item() * 2.0 ** -24 * 240 * max(2.0 ** exponent, 2.0 ** -118) if dtype == torch.bfloat16 else 0.0
+    tol = torch.finfo(dtype).eps / 2 * want.abs() + 2 * e * weight + lost + 300 * 2.0 ** -149
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
