@@ -615,16 +615,17 @@ __global__ void __launch_bounds__(kThreads, 2)
             tc_fence_before();
             const bool complete = walk.complete();
             float* part = a.part + (int64_t)(2 * blockIdx.x + (walk.first ? 0 : 1)) * part_stride<RC>();
+            const int lr = lane % RC;  // this lane's row
+            const float sum = ms.sums[0][lr] + ms.sums[1][lr] + ms.sums[2][lr] + ms.sums[3][lr];
+            const float inv = sum == 0.f ? 0.f : 1.f / sum, vref = power_of_two(-state.lrv);
+            if (!complete && tid < u.rows) part[RC * kD + tid] = state.m, part[RC * kD + RC + tid] = sum;
 #pragma unroll
             for (int r = 0; r < RC; ++r) {
                 if (r >= u.rows) continue;
-                const float m = __shfl_sync(kFull, state.m, r), vref = power_of_two(-__shfl_sync(kFull, state.lrv, r));
-                const float sum = ms.sums[0][r] + ms.sums[1][r] + ms.sums[2][r] + ms.sums[3][r];
-                float v = sum == 0.f ? 0.f : o[r] / sum * vref;
+                float v = o[r] * __shfl_sync(kFull, inv, r) * __shfl_sync(kFull, vref, r);
                 if ((ms.nan[r][tid >> 5] >> (tid & 31)) & 1u) v = NAN;
                 if (!complete) {
                     part[r * kD + tid] = v;
-                    if (tid == 0) part[RC * kD + r] = m, part[RC * kD + RC + r] = sum;
                     continue;
                 }
                 const int rr = u.r0 + r, i = (int)fdiv((uint32_t)rr, a.G);
