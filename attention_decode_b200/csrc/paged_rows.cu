@@ -173,10 +173,13 @@ struct RowState {
     float vref;        // reference of weight x v scale, relative to m; 0 before the first token
 };
 
-// The factor of a weight under a page's v scale. (A finite one: a weight of 0
-// stays 0. One that this holds down has passed kLag and raises the reference.)
-__device__ __forceinline__ float value_factor(float vs, const RowState& st) {
-    return vs == st.vref ? 1.f : fminf(__fdividef(vs, st.vref), 0x1p126f);
+// The factor of weights under a page's v scale. (A finite one: a weight of 0
+// stays 0. One that this holds down has passed kLag and raises the reference. The
+// scale of a page that was not loaded is void, but then no weight is seen.)
+__device__ __forceinline__ float value_factor(float vs, bool seen, float vref) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(vref));
+    return !seen ? 0.f : vs == vref ? 1.f : fminf(vs * inv, 0x1p126f);
 }
 
 // Multiplies a row's weights of the step so far (`done` columns of fp16 pairs) and,
@@ -228,10 +231,6 @@ __device__ __forceinline__ void row_weights(const uint32_t (&u)[16], uint32_t se
         if (WEIGH) {
             x.x *= w;
             x.y *= w;
-            if (MASKED) {  // the scale of a page that was not loaded is void
-                x.x = (seen >> i) & 1u ? x.x : 0.f;
-                x.y = (seen >> i) & 2u ? x.y : 0.f;
-            }
         }
         p[i / 2] = f16x2(x.x, x.y);
     }
@@ -295,7 +294,8 @@ __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, in
         const float2 kv = scale[col >> page_log];
         uint32_t u[16];
         TmemLoad<16>::run(s + 16 * q, u);
-        float most, sum, w = WEIGH ? value_factor(kv.y, st) : 1.f;
+        const bool some = !MASKED || (seen & 0xffffu);
+        float most, sum, w = WEIGH ? value_factor(kv.y, some, st.vref) : 1.f;
         uint32_t p[8];
         row_weights<MASKED, WEIGH>(u, seen, kv.x, w, st, most, sum, p);
         const bool need = real && (most > kBias + kLag || (WEIGH && w > 1.f && sum * w > kMost));
@@ -311,7 +311,7 @@ __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, in
             st.vref = r.y;
             st.l *= r.z;
             TmemLoad<16>::run(s + 16 * q, u);
-            if (WEIGH) w = value_factor(kv.y, st);
+            if (WEIGH) w = value_factor(kv.y, some, st.vref);
             row_weights<MASKED, WEIGH>(u, seen, kv.x, w, st, most, sum, p);
         }
         st.l += sum;
