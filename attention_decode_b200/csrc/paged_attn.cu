@@ -213,10 +213,10 @@ __device__ __forceinline__ RowState first_state(Misc& ms, int warp, int rows) {
     __syncwarp();
     return {r < rows ? -INFINITY : 0.f, 0.f, 0.f, 0.f};
 }
-// Rows' maxima raised to the tile's (ms.red) where the tile passes a lag. The e is the whole number below the
-// distance of the maxima (a little above it, for the rounding of their sum), so
-// that the largest w is between 2^kBias and twice that; its bounds keep p * 2^-e
-// finite.
+// Rows' maxima raised to the tile's (ms.red) where the tile passes a lag. The e is
+// the whole number below the distance of the maxima (or at most 1/16 above it, for
+// the rounding of their sum), so that the largest w is between 2^kBias and twice
+// that; its bounds keep p * 2^-e finite.
 template <int RC>
 __device__ __forceinline__ void raise_maxima(Misc& ms, int warp, RowState& st) {
     const int r = lane_id() % RC;

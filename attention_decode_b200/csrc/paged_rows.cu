@@ -207,8 +207,9 @@ __device__ __noinline__ void rescale_row(uint32_t s, int done, uint32_t o, bool 
 
 // Weights of 16 columns of a row from their scores u: exponents, the largest
 // of them, 2^x, their sum; packed in fp16 pairs, times w. WEIGH: some row's
-// reference is not the page's v scale (w may not be 1). (Exponents are formed in packed pairs, as the scores
-// lie; what follows 2^x is scalar: packing it again costs more moves than it saves.)
+// reference is not the page's v scale (w may not be 1). (Exponents are formed in
+// packed pairs, as the scores lie; what follows 2^x is scalar: packing it again
+// costs more moves than it saves.)
 template <bool MASKED, bool WEIGH>
 __device__ __forceinline__ void row_weights(const uint32_t (&u)[16], uint32_t seen, float ks, float w, const RowState& st,
                                             float& most, float& sum, uint32_t (&p)[8]) {
