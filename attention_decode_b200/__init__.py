@@ -708,7 +708,8 @@ def nsnq_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, page_
     rows [cu_rows[b], cu_rows[b+1]) (one row each without cu_rows), its last
     tokens: seq_lens[b] counts its tokens with them. page_table [B][columns]
     lists each sequence's pages. With q [rows][Hq][D], returns q rotated the
-    same way (into q_out if given; rows of no sequence are not written)."""
+    same way (into q_out if given, which may be a contiguous q itself; rows of no
+    sequence are not written)."""
     c, index, dtype = cache._c(), k.get_device(), k.dtype
     N, H, D = k.shape
     k_t, k_h, k_d = k.stride()
@@ -757,7 +758,7 @@ def nsnq_paged_attn(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     [rows][Hq][D]. max_rows bounds the rows of a sequence (without it, one row
     without cu_rows, all rows with them: give the real bound, small counts run on
     a faster kernel and need less workspace). Rows past max_rows and rows of no
-    sequence are not written. With window > 0 a row sees the last
+    sequence are not written; out must not overlap q. With window > 0 a row sees the last
     `window` tokens up to its own and the first `sinks`."""
     c, index = cache._c(), q.get_device()
     N, Hq, D = q.shape

@@ -78,6 +78,15 @@ nsnq_status check_rows(const void* p, const char* name, int64_t n_rows, int head
     return NSNQ_OK;
 }
 
+// Whether row tensor p (strides in elements of esz bytes) and the contiguous
+// output o have bytes in common. Blocks write rows while others still read.
+bool overlap(const void* p, int64_t n_rows, int heads, int64_t st, int64_t sh, int64_t esz, const void* o, int64_t rows,
+             int Ho, int64_t osz) {
+    const uintptr_t p0 = reinterpret_cast<uintptr_t>(p), o0 = reinterpret_cast<uintptr_t>(o);
+    const uintptr_t p1 = p0 + ((n_rows - 1) * st + (heads - 1) * sh + nsnq::kHeadDim) * esz;
+    return p0 < o0 + rows * Ho * nsnq::kHeadDim * osz && o0 < p1;
+}
+
 }  // namespace
 
 extern "C" {
@@ -108,6 +117,10 @@ nsnq_status nsnq_paged_append(const void* k, const void* v, const void* q, void*
         return set_error(NSNQ_ERR_INVALID_ARG, "q_out is NULL or not 16-byte aligned");
     if (q && q == q_out && ((n_rows > 1 && q_stride_t != (int64_t)Hq * D) || (Hq > 1 && q_stride_h != D)))
         return set_error(NSNQ_ERR_INVALID_ARG, "q_out may equal q only if q is contiguous");
+    if (q && (overlap(k, n_rows, Hkv, k_stride_t, k_stride_h, esz, q_out, n_rows, Hq, esz) ||
+              overlap(v, n_rows, Hkv, v_stride_t, v_stride_h, esz, q_out, n_rows, Hq, esz) ||
+              (q != q_out && overlap(q, n_rows, Hq, q_stride_t, q_stride_h, esz, q_out, n_rows, Hq, esz))))
+        return set_error(NSNQ_ERR_INVALID_ARG, "q_out overlaps k, v or (other than as a whole) q");
     a.k = k; a.v = v; a.q = q; a.q_out = q_out;
     a.k_st = k_stride_t; a.k_sh = k_stride_h;
     a.v_st = v_stride_t; a.v_sh = v_stride_h;
@@ -162,6 +175,9 @@ nsnq_status nsnq_paged_attn(const void* q, nsnq_dtype q_dtype, int64_t n_rows, i
                          workspace ? workspace_bytes : (size_t)0);
     if (!aligned(workspace, nsnq::kWsAlign))
         return set_error(NSNQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (overlap(q, n_rows, Hq, q_stride_t, q_stride_h, q_dtype == NSNQ_BF16 ? 2 : 4, out, n_rows, Hq,
+                out_dtype == NSNQ_BF16 ? 2 : 4))
+        return set_error(NSNQ_ERR_INVALID_ARG, "out overlaps q");
     a.q = q; a.q_bf16 = q_dtype == NSNQ_BF16;
     a.q_st = q_stride_t; a.q_sh = q_stride_h;
     a.max_rows = max_rows;

@@ -436,7 +436,7 @@ typedef enum {
  *          strides (elements; channels contiguous, rows 16-byte aligned).
  *   q      device [n_rows][Hq][D] likewise, or NULL: rotated like the keys
  *          into q_out [n_rows][Hq][D] (contiguous, of dtype; may equal a
- *          contiguous q). fp32: the fp64 value rounded once. bf16: the same
+ *          contiguous q, else it must not overlap q, k or v). fp32: the fp64 value rounded once. bf16: the same
  *          in calls of up to two rows per sequence on average; with more
  *          rows it is rotated in fp32, and a value within 2^-21 (|x_i| +
  *          |x_{i+D/2}|) of the middle between two bf16 numbers may become
@@ -484,7 +484,7 @@ size_t nsnq_paged_attn_workspace(int64_t n_rows, int B, int Hq, int Hkv, int D, 
  *   max_rows  host upper bound on the rows of a sequence.
  *   window 0: every token up to pos; else >= 1. sinks >= 0, used with window.
  *   softmax_scale  0 means 1/sqrt(D).
- *   out    device [n_rows][Hq][D] contiguous, out_dtype.
+ *   out    device [n_rows][Hq][D] contiguous, out_dtype; must not overlap q.
  *   workspace  >= nsnq_paged_attn_workspace(...) bytes, 256-byte aligned;
  *          calls that may run at the same time need one each.
  * Pages that no row of the call sees are not read and their table entries
