@@ -29,8 +29,10 @@
 // whole powers of two, is the e of w, so that w spans the pieces' range whatever
 // the scales are. The bias 2^kBias keeps the smallest piece at 2^-23 of the row's
 // largest w. Where every row's 2^e is the token's v scale (equal scales, powers of
-// two), w is p. A row's maxima move only for tokens that it sees itself: no bit of
-// a row depends on what it does not see.
+// two), w is p. No bit of a row depends on what it does not see: the unit's rows
+// raise their maxima together while all of them have seen the same tokens (rows of
+// one position, or whole tiles so far), from then on each by itself. (A raise holds
+// up the tile; rows that raise one by one do so in a fifth to a third more tiles.)
 //
 // What bounds it: memory for up to 4 rows (16 sequences x 32k tokens, 8
 // kv-heads, 4 query heads each: 166 us, 6.5 TB/s, 98 % of the measured copy
@@ -213,16 +215,17 @@ __device__ __forceinline__ RowState first_state(Misc& ms, int warp, int rows) {
     __syncwarp();
     return {r < rows ? -INFINITY : 0.f, 0.f, 0.f, 0.f};
 }
-// Rows' maxima raised to the tile's (ms.red) where the tile passes a lag. The e is
+// Rows' maxima raised to the tile's (ms.red), all of them or (joint: false) where
+// the tile passes a lag. The e is
 // the whole number below the distance of the maxima (or at most 1/16 above it, for
 // the rounding of their sum), so that the largest w is between 2^kBias and twice
 // that; its bounds keep p * 2^-e finite.
 template <int RC>
-__device__ __forceinline__ void raise_maxima(Misc& ms, int warp, RowState& st) {
+__device__ __forceinline__ void raise_maxima(Misc& ms, int warp, bool joint, RowState& st) {
     const int r = lane_id() % RC;
     const float top = fmaxf(fmaxf(ms.red[0][r].x, ms.red[1][r].x), fmaxf(ms.red[2][r].x, ms.red[3][r].x));
     const float top_w = fmaxf(fmaxf(ms.red[0][r].y, ms.red[1][r].y), fmaxf(ms.red[2][r].y, ms.red[3][r].y));
-    const bool need = top - st.m > kLag || top_w - st.m + st.lrv > kLag;
+    const bool need = (joint && top > -INFINITY) || top - st.m > kLag || top_w - st.m + st.lrv > kLag;
     const float mn = need ? fmaxf(st.m, top) : st.m, e0 = -st.lrv;
     const float e = need ? fminf(fmaxf(floorf(fmaxf(st.m + e0, top_w) - mn + 0.0625f), -118.f), 126.f) : e0;
     const float down = st.m == mn ? 0.f : st.m - mn;
@@ -457,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             bar_tokens();
             RowState state = first_state<RC>(ms, warp, u.rows);
             const float2* row_cb = ms.cb[warp];
+            bool joint = true;  // the rows have seen the same tokens of the segment
             float l[RC];
 #pragma unroll
             for (int r = 0; r < RC; ++r) l[r] = 0.f;
@@ -470,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t have = ms.ok[st];
                 const bool whole = have == all_slots && tile * kTile + kTile - 1 <= u.p0 &&
                                    (!a.window || tile * kTile > u.p1 - a.window || tile * kTile + kTile <= a.sinks);
+                joint &= whole || u.p0 == u.p1;
                 const float ks = ms.ks[st][slot], vs = ms.vs[st][slot];
                 uint32_t vis = real;
                 if (!whole) {
@@ -518,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (lane == 0) ms.red[warp][r] = make_float2(top, top_w);
                     }
                     bar_tokens();  // (red is written again behind the next vote at the earliest)
-                    raise_maxima<RC>(ms, warp, state);
+                    raise_maxima<RC>(ms, warp, joint, state);
                     float f[RC];
 #pragma unroll
                     for (int r = 0; r < RC; ++r) {

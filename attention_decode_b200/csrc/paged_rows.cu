@@ -18,9 +18,11 @@
 // What meets V's codes is a weight times its page's v scale, over a reference
 // of the row's own: the largest such product among the tokens that the row has
 // seen has a reference of its own lag and takes the range of fp16 as above,
-// whatever the scales are; the sum of the weights stays on their own maximum. A
-// row's maximum and reference move only for its own tokens, so no bit of a row
-// depends on what it does not see.
+// whatever the scales are; the sum of the weights stays on their own maximum. No
+// bit of a row depends on what it does not see: a warp's rows raise their maxima
+// together while all of them have seen the same tokens (every tile so far was
+// whole), from then on each by itself. (A raise holds up its half's P V; rows that
+// raise one by one do so at more steps: 8192 prompt 724 us.)
 //
 // What bounds it: a tile needs 2048 clocks of the tensor cores (2 halves x (S
 // 512 + P V 512)) and 2048 of the exponential unit (2 x 16384 at 16 a clock), and
@@ -287,7 +289,8 @@ __device__ __noinline__ float3 raise_row(uint32_t s, uint32_t o, bool have_o, in
 // of its own, and fetching longer code costs more than its overlap gains.)
 template <bool MASKED, bool WEIGH>
 __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, int b, const float2* scale, int page_log,
-                                         bool real, const View& view, RowState& st, Waiter& wait, uint32_t pv_done) {
+                                         bool real, bool joint, const View& view, RowState& st, Waiter& wait,
+                                         uint32_t pv_done) {
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
         const int col = 64 * b + 16 * q;
@@ -299,8 +302,9 @@ __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, in
         float most, sum, w = WEIGH ? value_factor(kv.y, some, st.vref) : 1.f;
         uint32_t p[8];
         row_weights<MASKED, WEIGH>(u, seen, kv.x, w, st, most, sum, p);
-        const bool need = real && (most > kBias + kLag || (WEIGH && w > 1.f && sum * w > kMost));
+        bool need = real && (most > kBias + kLag || (WEIGH && w > 1.f && sum * w > kMost));
         if (__any_sync(kFull, need)) {
+            need |= real && joint;
             if (have_o) {  // O is quiet once the step before is done; the one in
                            // front of that is, it came before these scores
                 wait(pv_done, b ^ 1);
@@ -571,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready[hf]));
                 RowState st{c, real ? -INFINITY : 0.f, 0.f, 0.f};
+                bool joint = true;  // the warp's rows have seen the same tokens of the segment
 #pragma unroll 1
                 for (int j = j0; j < j1; ++j, ++it, ++n) {
                     const uint32_t ring = it % kRing;
@@ -590,15 +595,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float vmin = __uint_as_float(__reduce_min_sync(
                         kFull, lane < slots && ((ok >> lane) & 1u) ? __float_as_uint(scale[lane].y) : 0x7f800000u));
                     const bool one = whole && vmin == vmax;  // one v scale in the tile
+                    joint &= whole;
 #pragma unroll 1
                     for (int b = 0; b < 2; ++b) {
                         wait(smem_u32(&ms.s_full[hf][b]), n & 1);
                         tc_fence_after();
                         const bool have_o = j > j0 || b > 0;
                         const bool plain = one && __all_sync(kFull, !real || vmax == st.vref);
-                        if (plain) row_step<false, false>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
-                        else if (whole) row_step<false, true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
-                        else row_step<true, true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, view, st, wait, pv_done);
+                        if (plain) row_step<false, false>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, joint, view, st, wait, pv_done);
+                        else if (whole) row_step<false, true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, joint, view, st, wait, pv_done);
+                        else row_step<true, true>(s_at + 64 * b, o_at, have_o, b, scale, page_log, real, joint, view, st, wait, pv_done);
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&ms.p_full[hf][b]));
