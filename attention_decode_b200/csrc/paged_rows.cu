@@ -274,7 +274,7 @@ __device__ __noinline__ float3 raise_row(uint32_t s, uint32_t o, bool have_o, in
         }
     }
     const float f = m == mn ? 1.f : exp2_approx(m - mn), old = vref * f;
-    vn = need ? fminf(fmaxf(fmaxf(old, vn), 0x1p-126f), 0x1p126f) : vref;
+    vn = need && mn > -INFINITY ? fminf(fmaxf(fmaxf(old, vn), 0x1p-126f), 0x1p126f) : vref;
     const float fo = vn == old ? 1.f : old / vn;
     if (__any_sync(kFull, fo != 1.f)) rescale_row(s, 8 * q, o, have_o, fo);
     return make_float3(mn, vn, f);
@@ -304,7 +304,9 @@ __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, in
         row_weights<MASKED, WEIGH>(u, seen, kv.x, w, st, most, sum, p);
         bool need = real && (most > kBias + kLag || (WEIGH && w > 1.f && sum * w > kMost));
         if (__any_sync(kFull, need)) {
-            need |= real && joint;
+            // (a row before its first token may take its maximum early: of the step's
+            // columns it is the same as behind the first one that it sees)
+            need |= real && (joint || st.m == -INFINITY);
             if (have_o) {  // O is quiet once the step before is done; the one in
                            // front of that is, it came before these scores
                 wait(pv_done, b ^ 1);
