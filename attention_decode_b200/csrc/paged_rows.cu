@@ -49,7 +49,7 @@ namespace {
 
 constexpr int RC = 256;         // rows of a unit
 constexpr int kThreads = 512;   // warps 0-3, 4-7: rows; 8-11: V to fp16; 12: TMA; 13: MMA issue
-constexpr float kLag = 16.75f, kBias = -1.f, kMost = 55108.f;  // kMost = 2^(kBias + kLag)
+constexpr float kLag = 16.75f, kBias = -1.f;
 constexpr int kKStages = 3, kRing = 8;
 constexpr int kMaxSlots = 8;
 // Tiles that a unit's queries and epilogue cost (2, 3, 5, 8: the 8192 prompt 795,
@@ -178,10 +178,21 @@ struct RowState {
 // The factor of weights under a page's v scale. (A finite one: a weight of 0
 // stays 0. One that this holds down has passed kLag and raises the reference. The
 // scale of a page that was not loaded is void, but then no weight is seen.)
-__device__ __forceinline__ float value_factor(float vs, bool seen, float vref) {
+__device__ __forceinline__ float reciprocal(float v) {
     float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(vref));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(v));
+    return inv;
+}
+__device__ __forceinline__ float value_factor(float vs, bool seen, float vref, float inv) {
     return !seen ? 0.f : vs == vref ? 1.f : fminf(vs * inv, 0x1p126f);
+}
+
+// The exponent that a weight may have under factor w: kBias + kLag, less the next
+// whole log2 of a w above 1. (Known before the exponentials: their sum, times w,
+// would do as well and comes later.)
+__device__ __forceinline__ float weight_limit(float w) {
+    const int n = max((int)((__float_as_uint(w) + 0x7fffffu) >> 23), 127);
+    return kBias + kLag + 127.f - (__uint_as_float(0x4b000000u + n) - 0x1p23f);
 }
 
 // Multiplies a row's weights of the step so far (`done` columns of fp16 pairs) and,
@@ -283,14 +294,15 @@ __device__ __noinline__ float3 raise_row(uint32_t s, uint32_t o, bool have_o, in
 // The weights of a row over step b of a tile (64 tokens), 16 columns at a time,
 // over the front of its scores: column pair i of P takes the place of score i,
 // which has been read by then. Where a row's largest exponent in a chunk passes
-// the lag, or its weights times the v scale may (their sum bounds them), the row's
-// maximum and reference are raised first. (Short loops: 32 columns at a time
+// the lag, or may pass it times w, the row's maximum and reference are raised
+// first. (Short loops: 32 columns at a time
 // took 2 % longer, 64 in a row 15 %: eight warps run this code each at a place
 // of its own, and fetching longer code costs more than its overlap gains.)
 template <bool MASKED, bool WEIGH>
 __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, int b, const float2* scale, int page_log,
                                          bool real, bool joint, const View& view, RowState& st, Waiter& wait,
                                          uint32_t pv_done) {
+    float inv = WEIGH ? reciprocal(st.vref) : 0.f;
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
         const int col = 64 * b + 16 * q;
@@ -299,10 +311,10 @@ __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, in
         uint32_t u[16];
         TmemLoad<16>::run(s + 16 * q, u);
         const bool some = !MASKED || (seen & 0xffffu);
-        float most, sum, w = WEIGH ? value_factor(kv.y, some, st.vref) : 1.f;
+        float most, sum, w = WEIGH ? value_factor(kv.y, some, st.vref, inv) : 1.f;
         uint32_t p[8];
         row_weights<MASKED, WEIGH>(u, seen, kv.x, w, st, most, sum, p);
-        bool need = real && (most > kBias + kLag || (WEIGH && w > 1.f && sum * w > kMost));
+        bool need = real && most > (WEIGH ? weight_limit(w) : kBias + kLag);
         if (__any_sync(kFull, need)) {
             // (a row before its first token may take its maximum early: of the step's
             // columns it is the same as behind the first one that it sees)
@@ -318,7 +330,10 @@ __device__ __forceinline__ void row_step(uint32_t s, uint32_t o, bool have_o, in
             st.vref = r.y;
             st.l *= r.z;
             TmemLoad<16>::run(s + 16 * q, u);
-            if (WEIGH) w = value_factor(kv.y, some, st.vref);
+            if (WEIGH) {
+                inv = reciprocal(st.vref);
+                w = value_factor(kv.y, some, st.vref, inv);
+            }
             row_weights<MASKED, WEIGH>(u, seen, kv.x, w, st, most, sum, p);
         }
         st.l += sum;
