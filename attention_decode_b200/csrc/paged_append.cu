@@ -16,7 +16,7 @@
 // per block, in shared memory, and serve all its heads. Queries are not decisions:
 // bf16 ones are rounded from the fp32 rotation (deciding again where that is not
 // sure of the nearest bf16 took 257 us instead of 181 below, for one bit in 3 *
-// 10^4 values), fp32 ones from one in two words (22 -> 25 us, 5 x ~580 rows).
+// 10^4 values), fp32 ones from one in two words (21 -> 23 us, 5 x ~580 rows).
 //
 // What bounds it: memory, in the end (a row is read once and written once; the
 // next heads' rows are copied to shared memory ahead by cp.async). A prompt of
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(AppShape<PAGE>::kThreads)
         for (int r = rg; r < last; r += kThreads / 8) {
             if (r < first) continue;
             float ch[8], cl[8], sh_[8], sl[8];
-#pragma unroll 1
+#pragma unroll 2
             for (int i = 0; i < 8; ++i) {
                 double s, c;
                 sincospi(2.0 * (t0 + r) * a.turns[8 * l + i], &s, &c);
