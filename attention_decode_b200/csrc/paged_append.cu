@@ -9,10 +9,10 @@
 //
 // Codes and scales are those of the fp64 rotation, decided in fp32: angles are
 // reduced in fp64, cos and sin rounded to fp32, and a rotated value is then
-// off by at most 2^-21.8 (|x| + |y|) of its pair (x, y): 2^-24 each for cos or sin
-// and its angle, the product and the sum. Where a code or scale
-// would change within twice that, it is decided again from an fp64 rotation
-// (about one code in 10^5). The cos and sin of a page's rows are computed once
+// off by at most 2^-21.8 (|x| + |y|) of its pair (x, y): the roundings of the angle,
+// of cos or sin, of a product and of the sum. Where a code or scale would change
+// within twice that, it is decided again from an fp64 rotation (about one code in
+// 10^5). The cos and sin of a page's rows are computed once
 // per block, in shared memory, and serve all its heads. Queries are not decisions:
 // bf16 ones are rounded from the fp32 rotation (deciding again where that is not
 // sure of the nearest bf16 took 257 us instead of 181 below, for one bit in 3 *
@@ -20,8 +20,8 @@
 //
 // What bounds it: memory, in the end (a row is read once and written once; the
 // next heads' rows are copied to shared memory ahead by cp.async). A prompt of
-// 8 x 4096 tokens, 8 kv-heads and 32 query heads, bf16 takes 180 us: 738 MB at
-// 4.1 TB/s (62 % of the measured copy rate). fp64 throughout took 498 us, fp32
+// 8 x 4096 tokens, 8 kv-heads and 32 query heads, bf16 takes 183 us: 738 MB at
+// 4.0 TB/s (61 % of the measured copy rate). fp64 throughout took 498 us, fp32
 // with one head's rows in flight 311, with the next head's in registers 196.
 //
 #include <math.h>

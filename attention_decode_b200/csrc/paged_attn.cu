@@ -35,11 +35,11 @@
 // up the tile; rows that raise one by one do so in a fifth to a third more tiles.)
 //
 // What bounds it: memory for up to 4 rows (16 sequences x 32k tokens, 8
-// kv-heads, 4 query heads each: 166 us, 6.5 TB/s, 98 % of the measured copy
-// rate); one 131k sequence 53 us (5.0 TB/s: start, join and the longer waits of
-// single pages weigh in). With 8 and 16 rows the token warps' work does: 64
-// sequences under a 2048 window, 8 heads 64 us (4.2 TB/s), 13 x 4 drafted rows
-// over ~6k tokens, 4 heads 55 us (2.9 TB/s). A lag of 2^3 instead of 2^5 raised
+// kv-heads, 4 query heads each: 165 to 169 us, 6.4 to 6.5 TB/s, 97 to 99 % of the
+// measured copy rate); one 131k sequence 54 us (5.0 TB/s: start, join and the longer
+// waits of single pages weigh in). With 8 and 16 rows the token warps' work does:
+// 64 sequences under a 2048 window, 8 heads 64 us (4.3 TB/s), 13 x 4 drafted rows
+// over ~6k tokens, 4 heads 53 us (3.0 TB/s). A lag of 2^3 instead of 2^5 raised
 // maxima in half of those tiles (69 us). One-CUDA-core-row-per-block attention,
 // the first version, took 6461 us for the 16 x 32k batch.
 #include <math.h>

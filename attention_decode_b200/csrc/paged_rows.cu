@@ -22,7 +22,7 @@
 // bit of a row depends on what it does not see: a warp's rows raise their maxima
 // together while all of them have seen the same tokens (every tile so far was
 // whole), from then on each by itself. (A raise holds up its half's P V; rows that
-// raise one by one do so at more steps: 8192 prompt 724 us.)
+// raise one by one do so at more steps: the 8192 prompt below took 724 us.)
 //
 // What bounds it: a tile needs 2048 clocks of the tensor cores (2 halves x (S
 // 512 + P V 512)) and 2048 of the exponential unit (2 x 16384 at 16 a clock), and
@@ -30,9 +30,9 @@
 // own chain (scores from TMEM, exponents, weights back, 64 tokens at a time) is
 // 1840 clocks long where the exponential unit alone would allow 512, and an SM
 // sub-partition has two such warps. Measured: a prompt of 8192 tokens, 32 query
-// heads on 8 kv-heads, causal, 713 us (771 TFLOP/s, 47 % of the measured bf16
-// rate); 447 + 280 rows behind 21.5k and 16.8k tokens 305 us (774 TFLOP/s);
-// 4 prompts of ~1500 under a 511 window with 5 sinks 146 us. On the way: scores
+// heads on 8 kv-heads, causal, 693 to 708 us (778 TFLOP/s, 47 % of the measured bf16
+// rate); 447 + 280 rows behind 21.5k and 16.8k tokens 292 to 308 us (774 TFLOP/s);
+// 4 prompts of ~1500 under a 511 window with 5 sinks 157 to 163 us. On the way: scores
 // in one go per tile 929 us, then 64-token steps with the next scores in flight
 // and MMA issue under elect (before, the issuing thread alone took 1700 clocks
 // per half and step) 749 us. Tried: two threads per row (794 us with, 822
