@@ -499,7 +499,8 @@ size_t nsnq_paged_attn_workspace(int64_t n_rows, int B, int Hq, int Hkv, int D, 
  * or by half a step of 2^-23 of the row's largest such product (of 2^-118, if
  * that is larger), whichever is more (the products, not the weights alone: a
  * token's share counts, not what scale its page has, nor the scales of pages
- * that the row does not see); with fp32 q or out, queries and weights keep 24
+ * that the row does not see). Weights below 2^-100 of the row's largest weight
+ * may vanish under any scale. With fp32 q or out, queries and weights keep 24
  * bits, at a several times lower rate for prompts. The same call gives the
  * same bits every time.
  */
