@@ -151,14 +151,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t a, const float* r) {
                  : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* u) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(a), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
-        "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* u) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
